@@ -22,7 +22,8 @@ namespace kda {
 constexpr int kDecodeThreads = 256;
 constexpr int kDecodeSlice = 64;  // columns of S per CTA
 
-template <typename TIn, int DK, bool GROUPED, bool PRO>
+// HEAD_GATE: one forget gate a head (log_alpha [N, H]) instead of one a key channel.
+template <typename TIn, int DK, bool GROUPED, bool PRO, bool HEAD_GATE = false>
 __global__ void __launch_bounds__(kDecodeThreads, 3)
 decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
                    const void* __restrict__ log_alpha, const float* __restrict__ beta, float* __restrict__ S,
@@ -51,7 +52,13 @@ decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const T
     const float b = (PRO && (pro & KDA_PROLOGUE_BETA_LOGITS)) ? sigmoid_f(beta[p]) : beta[p];
     const TIn* vp = v + (size_t)p * dv + j0 + 4 * cg;
     const float v0 = to_f32(vp[0]), v1 = to_f32(vp[1]), v2 = to_f32(vp[2]), v3 = to_f32(vp[3]);
+    const float a_head = HEAD_GATE ? expf(reinterpret_cast<const float*>(log_alpha)[p]) : 0.f;
     for (int c = tid; c < DK; c += kDecodeThreads) {
+        if (HEAD_GATE) {
+            s_k[c] = to_f32(k[(size_t)pq * DK + c]);
+            s_q[c] = to_f32(q[(size_t)pq * DK + c]);
+            continue;
+        }
         const size_t ia = (size_t)p * DK + c;  // gates fp32, or bf16 with the bf16-gate bit
         const float la = (PRO && (pro & KDA_PROLOGUE_GATE_BF16))
                              ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(log_alpha)[ia])
@@ -94,7 +101,7 @@ decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const T
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         const int c = rb + 16 * i;
-        const float a = s_a[c], kc = s_k[c], qc = s_q[c];
+        const float a = HEAD_GATE ? a_head : s_a[c], kc = s_k[c], qc = s_q[c];
         qk = fmaf(qc, kc, qk);  // rows rb + 16 i: the two half-warps together cover this warp's rows
         st[i].x *= a; st[i].y *= a; st[i].z *= a; st[i].w *= a;
         r0 = fmaf(st[i].x, kc, r0); r1 = fmaf(st[i].y, kc, r1); r2 = fmaf(st[i].z, kc, r2); r3 = fmaf(st[i].w, kc, r3);
@@ -178,6 +185,24 @@ cudaError_t launch_decode(const void* q, const void* k, const void* v, const voi
         else KDA_DECODE_LAUNCH(64, true, true);
     }
 #undef KDA_DECODE_LAUNCH
+    return cudaGetLastError();
+}
+
+// The step with one forget gate a head: the same pass over the state, no per-channel gates to read.
+template <typename TIn>
+cudaError_t launch_gdn_decode(const void* q, const void* k, const void* v, const float* la, const float* beta, float* S,
+                              void* out, int N, int H, int Hk, int dk, int dv, cudaStream_t stream)
+{
+    const long long blocks = (long long)N * H * (dv / kDecodeSlice);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    LaunchScope ls("gdn_decode_step", stream);
+    const int G = H / Hk;
+    auto* kern = dk == 128 ? (G == 1 ? decode_step_kernel<TIn, 128, false, false, true>
+                                     : decode_step_kernel<TIn, 128, true, false, true>)
+                           : (G == 1 ? decode_step_kernel<TIn, 64, false, false, true>
+                                     : decode_step_kernel<TIn, 64, true, false, true>);
+    kern<<<(unsigned)blocks, kDecodeThreads, 0, stream>>>((const TIn*)q, (const TIn*)k, (const TIn*)v, la, beta, S,
+                                                          (TIn*)out, dv, H, G, 0u);
     return cudaGetLastError();
 }
 

@@ -1,0 +1,54 @@
+// gdn.cuh -- the gated delta rule with one forget gate a head, on the CUDA-core chunk kernels.
+//
+// Every configuration the tensor-core kernels do not take (fp32, d = 64) runs here.  The per-channel
+// kernels hold the scalar gate as the special case of equal channels, so the gate is spread over the
+// dk channels into the workspace, and in the backward the channels' gate gradients are summed.
+#pragma once
+
+#include "common.cuh"
+#include "profile.cuh"
+
+namespace kda {
+
+__global__ void __launch_bounds__(256)
+gdn_spread_gate_kernel(const float* __restrict__ la, float4* __restrict__ out, long long n, int quads)
+{
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // a float4 of one (token, head)
+    if (i >= n) return;
+    const float a = la[i / quads];
+    out[i] = make_float4(a, a, a, a);
+}
+
+// one warp per (token, head): the sum over its dk channels, in a fixed order
+__global__ void __launch_bounds__(256)
+gdn_sum_gate_kernel(const float* __restrict__ dla, float* __restrict__ out, long long rows, int dk)
+{
+    const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    float s = 0.f;
+    for (int c = lane; c < dk; c += 32) s += dla[r * dk + c];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) out[r] = s;
+}
+
+inline cudaError_t launch_gdn_spread_gate(const float* la, float* out, long long rows, int dk, cudaStream_t stream)
+{
+    LaunchScope ls("gdn_spread_gate", stream);
+    const long long n = rows * (dk / 4), blocks = (n + 255) / 256;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    gdn_spread_gate_kernel<<<(unsigned)blocks, 256, 0, stream>>>(la, (float4*)out, n, dk / 4);
+    return cudaGetLastError();
+}
+
+inline cudaError_t launch_gdn_sum_gate(const float* dla, float* out, long long rows, int dk, cudaStream_t stream)
+{
+    LaunchScope ls("gdn_sum_gate", stream);
+    const long long blocks = (rows + 7) / 8;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    gdn_sum_gate_kernel<<<(unsigned)blocks, 256, 0, stream>>>(dla, out, rows, dk);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

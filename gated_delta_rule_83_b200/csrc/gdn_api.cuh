@@ -1,0 +1,197 @@
+// gdn_api.cuh -- C entry points of the scalar-gate delta rule and of the 8-bit state cache: argument
+// validation, workspace carving and dispatch (the end of kda_lib.cu's translation unit).
+#pragma once
+
+namespace {
+
+bool gdn_heads_ok(int H, int Hk) { return H > 0 && Hk > 0 && H % Hk == 0; }
+
+struct GdnFwdPlan {
+    Plan f;
+    size_t gate_bytes, slot_bytes, total;
+};
+
+kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, int num_seqs, kda_dtype dt,
+                             GdnFwdPlan& p)
+{
+    const kda_status st = make_plan(B, T, H, dk, dv, varlen, num_seqs, dt, p.f);
+    if (st != KDA_OK) return st;
+    p.gate_bytes = round_up(sizeof(float) * (size_t)p.f.Ttot * H * dk, kAlign);
+    p.slot_bytes = round_up(sizeof(float) * simt_slot_floats(dk, dv), kAlign);
+    p.total = sizeof(WsHeader) + p.f.off_bytes + p.gate_bytes + (size_t)p.f.max_chunks * H * p.slot_bytes;
+    return KDA_OK;
+}
+
+struct GdnBwdPlan {
+    BwdPlan b;
+    size_t gate_bytes, total;
+};
+
+kda_status make_gdn_bwd_plan(int B, int T, int H, int Hk, int dk, int dv, bool varlen, int num_seqs, kda_dtype dt,
+                             GdnBwdPlan& p)
+{
+    const kda_status st = make_bwd_plan(B, T, H, Hk, 0u, dk, dv, varlen, num_seqs, dt, p.b);
+    if (st != KDA_OK) return st;
+    p.gate_bytes = round_up(sizeof(float) * (size_t)p.b.f.Ttot * H * dk, kAlign);
+    p.total = round_up(p.b.total_bytes, kAlign) + 2 * p.gate_bytes;
+    return KDA_OK;
+}
+
+bool all_aligned16(std::initializer_list<const void*> ptrs)
+{
+    for (const void* x : ptrs)
+        if (x && !aligned16(x)) return false;
+    return true;
+}
+
+}  // namespace
+
+extern "C" kda_status kda_gdn_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, int varlen, int num_seqs,
+                                                       kda_dtype dt, size_t* bytes)
+{
+    if (!bytes) return KDA_ERR_INVALID_ARG;
+    GdnFwdPlan p;
+    const kda_status st = make_gdn_fwd_plan(B, T, H, dk, dv, varlen != 0, num_seqs, dt, p);
+    if (st != KDA_OK) return st;
+    *bytes = p.total;
+    return KDA_OK;
+}
+
+extern "C" kda_status kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const float* log_alpha,
+                                        const float* beta, const float* S0, const int32_t* cu_seqlens, int num_seqs,
+                                        void* out, float* S_final, int B, int T, int H, int Hk, int dk, int dv,
+                                        kda_dtype dt, void* workspace, size_t workspace_bytes, kda_stream_t stream_)
+{
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (!gdn_heads_ok(H, Hk)) return KDA_ERR_INVALID_ARG;
+    GdnFwdPlan p;
+    const kda_status st = make_gdn_fwd_plan(B, T, H, dk, dv, cu_seqlens != nullptr, num_seqs, dt, p);
+    if (st != KDA_OK) return st;
+    if (p.f.Ttot > 0 && (!q || !k || !v || !log_alpha || !beta || !out)) return KDA_ERR_INVALID_ARG;
+    if (!all_aligned16({q, k, v, S0, out, S_final}) || ((uintptr_t)log_alpha & 3u) || ((uintptr_t)beta & 3u) ||
+        ((uintptr_t)cu_seqlens & 3u))
+        return KDA_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace % kAlign) || workspace_bytes < p.total) return KDA_ERR_WORKSPACE;
+    char* ws = (char*)workspace;
+    WsHeader* hdr = (WsHeader*)ws;
+    int* off = (int*)(ws + sizeof(WsHeader));
+    {
+        LaunchScope ls("chunk_table", stream);
+        chunk_table_kernel<<<1, kTableThreads, 0, stream>>>(cu_seqlens, p.f.N, p.f.Tseq, p.f.Ttot, hdr, off,
+                                                            off + p.f.N + 1);
+        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+    }
+    float* gate = (float*)(ws + sizeof(WsHeader) + p.f.off_bytes);
+    float* slots = (float*)((char*)gate + p.gate_bytes);
+    cudaError_t e = cudaSuccess;
+    if (p.f.Ttot > 0) e = launch_gdn_spread_gate(log_alpha, gate, p.f.Ttot * H, dk, stream);
+    if (e == cudaSuccess)
+        e = dt == KDA_BF16 ? launch_simt_prefill<__nv_bfloat16>(q, k, v, gate, beta, S0, S_final, out, hdr, off,
+                                                                cu_seqlens, p.f.Tseq, p.f.N, H, Hk, 0u, dk, dv,
+                                                                p.f.max_chunks, slots, stream)
+                           : launch_simt_prefill<float>(q, k, v, gate, beta, S0, S_final, out, hdr, off, cu_seqlens,
+                                                        p.f.Tseq, p.f.N, H, Hk, 0u, dk, dv, p.f.max_chunks, slots,
+                                                        stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status kda_gdn_chunk_bwd_workspace_size(int B, int T, int H, int Hk, int dk, int dv, int varlen,
+                                                       int num_seqs, kda_dtype dt, size_t* bytes)
+{
+    if (!bytes || !gdn_heads_ok(H, Hk)) return KDA_ERR_INVALID_ARG;
+    GdnBwdPlan p;
+    const kda_status st = make_gdn_bwd_plan(B, T, H, Hk, dk, dv, varlen != 0, num_seqs, dt, p);
+    if (st != KDA_OK) return st;
+    *bytes = p.total;
+    return KDA_OK;
+}
+
+extern "C" kda_status kda_gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* log_alpha,
+                                        const float* beta, const float* S0, const int32_t* cu_seqlens, int num_seqs,
+                                        const void* dout, const float* dS_final, void* dq, void* dk_out, void* dv_out,
+                                        float* dlog_alpha, float* dbeta, float* dS0, int B, int T, int H, int Hk,
+                                        int dk, int dv, kda_dtype dt, void* workspace, size_t workspace_bytes,
+                                        kda_stream_t stream_)
+{
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (!gdn_heads_ok(H, Hk)) return KDA_ERR_INVALID_ARG;
+    GdnBwdPlan p;
+    const kda_status st = make_gdn_bwd_plan(B, T, H, Hk, dk, dv, cu_seqlens != nullptr, num_seqs, dt, p);
+    if (st != KDA_OK) return st;
+    const long long Ttot = p.b.f.Ttot;
+    if (Ttot > 0 && (!q || !k || !v || !log_alpha || !beta || !dout || !dq || !dk_out || !dv_out || !dlog_alpha ||
+                     !dbeta))
+        return KDA_ERR_INVALID_ARG;
+    if (!all_aligned16({q, k, v, S0, dout, dS_final, dq, dk_out, dv_out, dS0}) || ((uintptr_t)log_alpha & 3u) ||
+        ((uintptr_t)beta & 3u) || ((uintptr_t)dlog_alpha & 3u) || ((uintptr_t)dbeta & 3u) ||
+        ((uintptr_t)cu_seqlens & 3u))
+        return KDA_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace % kAlign) || workspace_bytes < p.total) return KDA_ERR_WORKSPACE;
+    float* gate = (float*)((char*)workspace + round_up(p.b.total_bytes, kAlign));
+    float* dgate = (float*)((char*)gate + p.gate_bytes);
+    if (Ttot > 0 && launch_gdn_spread_gate(log_alpha, gate, Ttot * H, dk, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    kda_options opt{};
+    opt.num_qk_heads = Hk;
+    const kda_status sb = kda_chunk_bwd(q, k, v, gate, beta, S0, cu_seqlens, num_seqs, dout, dS_final, dq, dk_out,
+                                        dv_out, dgate, dbeta, dS0, B, T, H, dk, dv, dt, &opt, workspace,
+                                        p.b.total_bytes, stream_);
+    if (sb != KDA_OK) return sb;
+    if (Ttot > 0 && launch_gdn_sum_gate(dgate, dlog_alpha, Ttot * H, dk, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    return KDA_OK;
+}
+
+extern "C" kda_status kda_gdn_decode_step(const void* q, const void* k, const void* v, const float* log_alpha,
+                                          const float* beta, float* S_inout, void* out, int N, int H, int Hk, int dk,
+                                          int dv, kda_dtype dt, kda_stream_t stream_)
+{
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (dt != KDA_BF16 && dt != KDA_F32) return KDA_ERR_INVALID_ARG;
+    if (N < 0 || dk <= 0 || dv <= 0 || !gdn_heads_ok(H, Hk)) return KDA_ERR_INVALID_ARG;
+    if (!dims_supported(dk, dv)) return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return KDA_OK;
+    if (!q || !k || !v || !log_alpha || !beta || !S_inout || !out) return KDA_ERR_INVALID_ARG;
+    if (!all_aligned16({q, k, v, S_inout, out}) || ((uintptr_t)log_alpha & 3u) || ((uintptr_t)beta & 3u))
+        return KDA_ERR_INVALID_ARG;
+    const cudaError_t e = dt == KDA_BF16
+        ? launch_gdn_decode<__nv_bfloat16>(q, k, v, log_alpha, beta, S_inout, out, N, H, Hk, dk, dv, stream)
+        : launch_gdn_decode<float>(q, k, v, log_alpha, beta, S_inout, out, N, H, Hk, dk, dv, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+namespace {
+
+kda_status check_cache_args(const void* S, const void* cache, const void* scale, const int32_t* slots, int N,
+                            int num_slots, int H, int dk, int dv)
+{
+    if (N < 0 || num_slots < 0 || H <= 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID_ARG;
+    if (!dims_supported(dk, dv)) return KDA_ERR_UNSUPPORTED;
+    if ((long long)H * dk > 65535LL * 32) return KDA_ERR_UNSUPPORTED;  // the grid's second axis
+    if (N == 0) return KDA_OK;
+    if (!S || !slots || (num_slots > 0 && (!cache || !scale))) return KDA_ERR_INVALID_ARG;
+    if (!all_aligned16({S, cache}) || ((uintptr_t)scale & 3u) || ((uintptr_t)slots & 3u)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" kda_status kda_state_cache_write(const float* S, int8_t* cache, float* scale, const int32_t* slots, int N,
+                                            int num_slots, int H, int dk, int dv, kda_stream_t stream_)
+{
+    const kda_status st = check_cache_args(S, cache, scale, slots, N, num_slots, H, dk, dv);
+    if (st != KDA_OK || N == 0) return st;
+    return launch_state_cache_write(S, cache, scale, slots, N, num_slots, H * dk, dv, (cudaStream_t)stream_) ==
+                   cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status kda_state_cache_read(const int8_t* cache, const float* scale, const int32_t* slots, float* S,
+                                           int N, int num_slots, int H, int dk, int dv, kda_stream_t stream_)
+{
+    const kda_status st = check_cache_args(S, cache, scale, slots, N, num_slots, H, dk, dv);
+    if (st != KDA_OK || N == 0) return st;
+    return launch_state_cache_read(cache, scale, slots, S, N, num_slots, H * dk, dv, (cudaStream_t)stream_) ==
+                   cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}

@@ -3,6 +3,7 @@
 // included below; this file only checks arguments and launches.
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <memory>
 #include <mutex>
 #include <vector>
@@ -14,9 +15,11 @@
 #include "chunks.cuh"
 #include "decode.cuh"
 #include "gated_norm.cuh"
+#include "gdn.cuh"
 #include "prefill_simt.cuh"
 #include "prefill_tc.cuh"
 #include "profile.cuh"
+#include "state_cache.cuh"
 
 using namespace kda;
 
@@ -707,3 +710,5 @@ extern "C" kda_status kda_chunk_fwd_host(const void* q, const void* k, const voi
     if (ok) rs = KDA_OK;
     return rs;
 }
+
+#include "gdn_api.cuh"

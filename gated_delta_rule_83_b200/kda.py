@@ -7,6 +7,7 @@ and importing a missing or unbuilt library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -66,6 +67,14 @@ ABI = {
     "kda_chunk_fwd_host": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.POINTER(KdaOptions),
                                 _I, _P, _SZ, _P]),
     "kda_host_release": (_I, []),
+    "kda_gdn_chunk_fwd_workspace_size": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "kda_gdn_chunk_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),
+    "kda_gdn_chunk_bwd_workspace_size": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "kda_gdn_chunk_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                               _I, _I, _P, _SZ, _P]),
+    "kda_gdn_decode_step": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "kda_state_cache_write": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "kda_state_cache_read": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "kda_check": (_I, [_P]),
     "kda_selftest_timeout": (_I, [_P]),
     "kda_profile_begin": (_I, []),
@@ -543,6 +552,226 @@ def gated_rmsnorm(o: torch.Tensor, z: torch.Tensor, weight: Optional[torch.Tenso
     rc = lib.kda_gated_rmsnorm(_ptr(o), _ptr(z), _ptr(weight), _ptr(out), rows, d, group, eps, act, _dt(o),
                                _stream_handle(stream, dev))
     _check("kda_gated_rmsnorm", rc)
+    return out
+
+
+@contextlib.contextmanager
+def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
+    """Device and stream of a call: outputs and workspaces allocated inside belong to the launch stream,
+    and the tensors' device is current for the launches.  Yields the stream handle."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    if stream is None and torch.cuda.current_device() == dev.index:
+        yield torch.cuda.current_stream(dev).cuda_stream
+    elif stream is None:
+        with torch.cuda.device(dev):
+            yield torch.cuda.current_stream(dev).cuda_stream
+    else:
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _shape(t: torch.Tensor, name: str, want):
+    if tuple(t.shape) != tuple(want):
+        raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
+
+
+def _given(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> torch.Tensor:
+    """An output the caller gave, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _req(t, name, dtype, dev)
+    _shape(t, name, shape)
+    return t
+
+
+def _gdn_inputs(q, k, v, log_alpha, beta, cu_seqlens, states):
+    """Checks shared by the chunked forward and backward; (B, T, H, Hk, dk, dv, N)."""
+    _req(q, "q")
+    dev = q.device
+    _dt(q)
+    if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("q must be [B, T, Hk, dk] and v [B, T, H, dv]")
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    for t, name, dt, shape in ((k, "k", q.dtype, q.shape), (v, "v", q.dtype, (B, T, H, dv)),
+                               (log_alpha, "log_alpha", torch.float32, (B, T, H)),
+                               (beta, "beta", torch.float32, (B, T, H))):
+        _req(t, name, dt, dev)
+        _shape(t, name, shape)
+    if Hk == 0 or H % Hk != 0:
+        raise ValueError(f"v's {H} heads must be a multiple of q's and k's {Hk}")
+    N = B
+    if cu_seqlens is not None:
+        _req(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if B != 1 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("packed varlen input needs B == 1 and cu_seqlens of N + 1 offsets")
+        N = cu_seqlens.numel() - 1
+    for t, name in states:
+        if t is not None:
+            _req(t, name, torch.float32, dev)
+            _shape(t, name, (N, H, dk, dv))
+    return B, T, H, Hk, dk, dv, N
+
+
+def _gdn_workspace(given: Optional[torch.Tensor], nbytes: int, dev) -> torch.Tensor:
+    """The caller's workspace, or one allocated for this call on the launch stream: it returns to the
+    allocator after the launches, so calls on other streams and captured graphs never share it."""
+    if given is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    _req(given, "workspace", torch.uint8, dev)
+    return given
+
+
+def gdn_workspace_size(B: int, T: int, H: int, dk: int, dv: int, varlen: bool = False, num_seqs: int = 0,
+                       dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace ``gdn_chunk_fwd`` needs (``kda_gdn_chunk_fwd_workspace_size``)."""
+    n = ctypes.c_size_t(0)
+    dt = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    _check("kda_gdn_chunk_fwd_workspace_size",
+           load_library().kda_gdn_chunk_fwd_workspace_size(B, T, H, dk, dv, int(bool(varlen)), num_seqs, dt,
+                                                           ctypes.byref(n)))
+    return n.value
+
+
+def gdn_bwd_workspace_size(B: int, T: int, H: int, dk: int, dv: int, varlen: bool = False, num_seqs: int = 0,
+                           dtype: torch.dtype = torch.bfloat16, qk_heads: Optional[int] = None) -> int:
+    """Bytes of workspace ``gdn_chunk_bwd`` needs (``kda_gdn_chunk_bwd_workspace_size``)."""
+    n = ctypes.c_size_t(0)
+    dt = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    _check("kda_gdn_chunk_bwd_workspace_size",
+           load_library().kda_gdn_chunk_bwd_workspace_size(B, T, H, qk_heads or H, dk, dv, int(bool(varlen)), num_seqs,
+                                                           dt, ctypes.byref(n)))
+    return n.value
+
+
+def gdn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: torch.Tensor, beta: torch.Tensor,
+                  S0: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, S_final: Optional[torch.Tensor] = None,
+                  output_final_state: bool = True, workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Chunked prefill of the gated delta rule with one forget gate a head (``kda_gdn_chunk_fwd``).
+
+    q, k: [B, T, Hk, dk]; v: [B, T, H, dv] (bf16 or fp32, H a multiple of Hk: value head h reads q/k head
+    h // (H // Hk)); log_alpha, beta: [B, T, H] fp32.  S0 / S_final: [N, H, dk, dv] fp32 (N = B, or
+    len(cu_seqlens) - 1 for packed input with B = 1); S_final may be S0 (in place).
+    Returns (out [B, T, H, dv] in q's dtype, S_final or None)."""
+    B, T, H, Hk, dk, dv, N = _gdn_inputs(q, k, v, log_alpha, beta, cu_seqlens, ((S0, "S0"),))
+    lib, dev, dt = load_library(), q.device, _dt(q)
+    with _on(dev, stream) as sh:
+        out = _given(out, "out", (B, T, H, dv), q.dtype, dev)
+        if S_final is not None or output_final_state:
+            S_final = _given(S_final, "S_final", (N, H, dk, dv), torch.float32, dev)
+        workspace = _gdn_workspace(workspace, gdn_workspace_size(B, T, H, dk, dv, cu_seqlens is not None, N, q.dtype),
+                                   dev)
+        _check("kda_gdn_chunk_fwd",
+               lib.kda_gdn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(S0),
+                                     _ptr(cu_seqlens), N, _ptr(out), _ptr(S_final), B, T, H, Hk, dk, dv, dt,
+                                     _ptr(workspace), workspace.numel(), sh))
+    return out, S_final
+
+
+def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: torch.Tensor, beta: torch.Tensor,
+                  dout: torch.Tensor, S0: Optional[torch.Tensor] = None, dS_final: Optional[torch.Tensor] = None,
+                  cu_seqlens: Optional[torch.Tensor] = None, want_dS0: bool = True, grads: Optional[dict] = None,
+                  workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Backward pass of ``gdn_chunk_fwd`` (``kda_gdn_chunk_bwd``): the derivatives of
+    ``L = sum(dout * out) + sum(dS_final * S_final)`` with respect to every input.
+
+    Inputs as ``gdn_chunk_fwd``, ``dout`` as its ``out``, ``dS_final`` [N, H, dk, dv] fp32 or None.
+    Returns a dict ``dq, dk, dv`` (dtype of q; dq and dk with Hk heads), ``dlog_alpha, dbeta`` (fp32) and
+    ``dS0`` (fp32, None when ``want_dS0`` is False).  ``grads`` may hold preallocated outputs under
+    those keys."""
+    B, T, H, Hk, dk, dv, N = _gdn_inputs(q, k, v, log_alpha, beta, cu_seqlens, ((S0, "S0"), (dS_final, "dS_final")))
+    lib, dev, dt = load_library(), q.device, _dt(q)
+    _req(dout, "dout", q.dtype, dev)
+    _shape(dout, "dout", (B, T, H, dv))
+    want = {"dq": (q.shape, q.dtype), "dk": (q.shape, q.dtype), "dv": (v.shape, q.dtype),
+            "dlog_alpha": ((B, T, H), torch.float32), "dbeta": ((B, T, H), torch.float32)}
+    if want_dS0:
+        want["dS0"] = ((N, H, dk, dv), torch.float32)
+    given = grads or {}
+    g = {"dS0": None}
+    with _on(dev, stream) as sh:
+        for key, (shape, kind) in want.items():
+            g[key] = _given(given.get(key), key, shape, kind, dev)
+        workspace = _gdn_workspace(
+            workspace, gdn_bwd_workspace_size(B, T, H, dk, dv, cu_seqlens is not None, N, q.dtype, Hk), dev)
+        _check("kda_gdn_chunk_bwd",
+               lib.kda_gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(S0),
+                                     _ptr(cu_seqlens), N, _ptr(dout), _ptr(dS_final), _ptr(g["dq"]), _ptr(g["dk"]),
+                                     _ptr(g["dv"]), _ptr(g["dlog_alpha"]), _ptr(g["dbeta"]), _ptr(g["dS0"]), B, T, H,
+                                     Hk, dk, dv, dt, _ptr(workspace), workspace.numel(), sh))
+    return g
+
+
+def gdn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: torch.Tensor, beta: torch.Tensor,
+                    S: torch.Tensor, out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One token of that recurrence for each of N sequences (``kda_gdn_decode_step``); ``S``
+    [N, H, dk, dv] fp32 is updated in place.  q, k: [N, Hk, dk]; v: [N, H, dv]; log_alpha, beta:
+    [N, H] fp32.  Returns out [N, H, dv]."""
+    _req(q, "q")
+    dev, dt = q.device, _dt(q)
+    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("q must be [N, Hk, dk] and v [N, H, dv]")
+    N, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    for t, name, kind, shape in ((k, "k", q.dtype, q.shape), (v, "v", q.dtype, (N, H, dv)),
+                                 (log_alpha, "log_alpha", torch.float32, (N, H)),
+                                 (beta, "beta", torch.float32, (N, H)), (S, "S", torch.float32, (N, H, dk, dv))):
+        _req(t, name, kind, dev)
+        _shape(t, name, shape)
+    if Hk == 0 or H % Hk != 0:
+        raise ValueError(f"v's {H} heads must be a multiple of q's and k's {Hk}")
+    with _on(dev, stream) as sh:
+        out = _given(out, "out", (N, H, dv), q.dtype, dev)
+        _check("kda_gdn_decode_step",
+               load_library().kda_gdn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(S),
+                                                  _ptr(out), N, H, Hk, dk, dv, dt, sh))
+    return out
+
+
+def _cache_args(cache, scale, slots):
+    _req(cache, "cache", torch.int8)
+    dev = cache.device
+    if cache.dim() != 4:
+        raise ValueError("cache must be [num_slots, H, dk, dv]")
+    _req(scale, "scale", torch.float32, dev)
+    _shape(scale, "scale", cache.shape[:3])
+    _req(slots, "slots", torch.int32, dev)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [N]")
+    return (dev, slots.numel(), *cache.shape)
+
+
+def state_cache_write(S: torch.Tensor, cache: torch.Tensor, scale: torch.Tensor, slots: torch.Tensor,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantise states into slots of an 8-bit cache (``kda_state_cache_write``): S [N, H, dk, dv] fp32,
+    cache [num_slots, H, dk, dv] int8, scale [num_slots, H, dk] fp32, slots [N] int32.  scale =
+    max |row| / 127, code = round(row / scale), ties to even.  A negative slot skips its state; of
+    states that name the same slot the last is kept; a slot past the cache is skipped and reported by
+    ``check()``."""
+    dev, N, num_slots, H, dk, dv = _cache_args(cache, scale, slots)
+    _req(S, "S", torch.float32, dev)
+    _shape(S, "S", (N, H, dk, dv))
+    with _on(dev, stream) as sh:
+        _check("kda_state_cache_write",
+               load_library().kda_state_cache_write(_ptr(S), _ptr(cache), _ptr(scale), _ptr(slots), N, num_slots, H,
+                                                    dk, dv, sh))
+
+
+def state_cache_read(cache: torch.Tensor, scale: torch.Tensor, slots: torch.Tensor,
+                     out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Read states back from slots of an 8-bit cache (``kda_state_cache_read``): code * scale as
+    [N, H, dk, dv] fp32, ready as ``S0`` or as a decode state.  A negative slot gives a zero state; a slot
+    past the cache does too and is reported by ``check()``; slots may repeat."""
+    dev, N, num_slots, H, dk, dv = _cache_args(cache, scale, slots)
+    with _on(dev, stream) as sh:
+        out = _given(out, "out", (N, H, dk, dv), torch.float32, dev)
+        _check("kda_state_cache_read",
+               load_library().kda_state_cache_read(_ptr(cache), _ptr(scale), _ptr(slots), _ptr(out), N, num_slots, H,
+                                                   dk, dv, sh))
     return out
 
 

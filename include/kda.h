@@ -332,6 +332,77 @@ kda_status kda_chunk_fwd_gated(const void* q, const void* k, const void* v, cons
                                kda_stream_t stream);
 
 /*
+ * kda_gdn_chunk_fwd -- chunked prefill of the gated delta rule with ONE forget gate a head:
+ *
+ *     S_t = alpha_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,     o_t = S_t^T q_t
+ *
+ * with alpha_t = exp(log_alpha_t) a scalar for each (token, head).  The attention review's GDN
+ * pseudo-code (lanjinlin.com.cn, entry on Qwen3-Next GDN: the state decayed by a scalar exp(g_t), then
+ * the delta correction) is this form; kda_chunk_fwd is the one with a gate for each key channel.
+ *
+ *   q, k       [B, T, Hk, dk] dt;  v [B, T, H, dv] dt: value head h reads q/k head h / (H / Hk).  H must
+ *              be a multiple of Hk.
+ *   log_alpha, beta  [B, T, H] fp32 (4-byte aligned; log_alpha <= 0 expected).
+ *   S0, cu_seqlens, num_seqs, out, S_final: as kda_chunk_fwd (S_final may alias S0).
+ * Accuracy: sums and states are fp32, and every fp32 operand of a tensor-core product is split into two
+ * bf16 parts (about 16 significant bits), so S_final is good to about 1e-5 for bf16 inputs as well.
+ * Supported: dk, dv in {64, 128}; any T >= 0.  Workspace, errors and asynchrony as kda_chunk_fwd.
+ */
+kda_status kda_gdn_chunk_fwd_workspace_size(int B, int T, int H, int dk, int dv, int varlen, int num_seqs,
+                                            kda_dtype dt, size_t* bytes);
+kda_status kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const float* log_alpha, const float* beta,
+                             const float* S0, const int32_t* cu_seqlens, int num_seqs, void* out, float* S_final,
+                             int B, int T, int H, int Hk, int dk, int dv, kda_dtype dt, void* workspace,
+                             size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_gdn_chunk_bwd -- the gradients of kda_gdn_chunk_fwd's inputs for the cotangents of its outputs:
+ * with L = sum(dout * out) + sum(dS_final * S_final),
+ *   dq, dk [B, T, Hk, dk] dt (summed over the value heads of a q/k head);  dv [B, T, H, dv] dt;
+ *   dlog_alpha, dbeta [B, T, H] fp32;  dS0 [N, H, dk, dv] fp32 or NULL (not wanted).  All written whole.
+ *   dout is [B, T, H, dv] dt; dS_final [N, H, dk, dv] fp32 or NULL (= 0).  The other arguments are those
+ * of the forward call.  No output may overlap an input.  Workspace, errors and asynchrony as
+ * kda_chunk_bwd.
+ */
+kda_status kda_gdn_chunk_bwd_workspace_size(int B, int T, int H, int Hk, int dk, int dv, int varlen, int num_seqs,
+                                            kda_dtype dt, size_t* bytes);
+kda_status kda_gdn_chunk_bwd(const void* q, const void* k, const void* v, const float* log_alpha, const float* beta,
+                             const float* S0, const int32_t* cu_seqlens, int num_seqs, const void* dout,
+                             const float* dS_final, void* dq, void* dk, void* dv, float* dlog_alpha, float* dbeta,
+                             float* dS0, int B, int T, int H, int Hk, int dk_dim, int dv_dim, kda_dtype dt,
+                             void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_gdn_decode_step -- one token of that recurrence for each of N sequences, the state updated in
+ * place: q, k [N, Hk, dk] dt; v, out [N, H, dv] dt; log_alpha, beta [N, H] fp32; S_inout [N, H, dk, dv]
+ * fp32.  Otherwise as kda_decode_step.
+ */
+kda_status kda_gdn_decode_step(const void* q, const void* k, const void* v, const float* log_alpha,
+                               const float* beta, float* S_inout, void* out, int N, int H, int Hk, int dk, int dv,
+                               kda_dtype dt, kda_stream_t stream);
+
+/*
+ * kda_state_cache_write / kda_state_cache_read -- recurrent states (of either gate form) put aside in
+ * slots of an 8-bit cache and read back: requests that are preempted and resumed, or that start from
+ * the state of a shared prefix, at a quarter of the fp32 states' memory.
+ *
+ *   S      [N, H, dk, dv] fp32 (read by write, written whole by read).
+ *   cache  [num_slots, H, dk, dv] int8;  scale [num_slots, H, dk] fp32, one for each row of dv values.
+ *   slots  [N] int32 on the device: the slot of each state.
+ * Write: scale = max |row| / 127, code = row / scale rounded to the nearest integer, ties to even (both
+ * divisions IEEE fp32); a row of zeros has scale 0; a row that holds an infinity or a NaN has scale NaN.
+ * Read: S = code * scale.  So a finite value comes back within scale / 2.
+ * A negative slot is "none": write skips that state and read returns zeros for it.  A slot >= num_slots
+ * does the same and records KDA_ERR_INVALID_ARG for kda_check().  Where `slots` names a slot twice, write
+ * keeps the state that comes later; read may name one as often as it likes.  Other slots are untouched.
+ * Supported: dk, dv in {64, 128}; N >= 0.  S and cache 16-byte aligned, scale and slots 4-byte.
+ */
+kda_status kda_state_cache_write(const float* S, int8_t* cache, float* scale, const int32_t* slots, int N,
+                                 int num_slots, int H, int dk, int dv, kda_stream_t stream);
+kda_status kda_state_cache_read(const int8_t* cache, const float* scale, const int32_t* slots, float* S, int N,
+                                int num_slots, int H, int dk, int dv, kda_stream_t stream);
+
+/*
  * kda_check -- synchronise `stream`, then read and clear the device error word of the current
  * device.  Returns KDA_OK, KDA_ERR_CUDA (a sticky CUDA error), KDA_ERR_BAD_SEQLENS or
  * KDA_ERR_TIMEOUT.
