@@ -6,8 +6,12 @@ namespace {
 
 bool gdn_heads_ok(int H, int Hk) { return H > 0 && Hk > 0 && H % Hk == 0; }
 
+// bf16 with dk = dv = 128 runs on the tensor cores, everything else on the CUDA-core chunk kernels
+bool gdn_use_tc(kda_dtype dt, int dk, int dv) { return dt == KDA_BF16 && dk == 128 && dv == 128; }
+
 struct GdnFwdPlan {
     Plan f;
+    bool tc;
     size_t gate_bytes, slot_bytes, total;
 };
 
@@ -16,8 +20,9 @@ kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, i
 {
     const kda_status st = make_plan(B, T, H, dk, dv, varlen, num_seqs, dt, p.f);
     if (st != KDA_OK) return st;
-    p.gate_bytes = round_up(sizeof(float) * (size_t)p.f.Ttot * H * dk, kAlign);
-    p.slot_bytes = round_up(sizeof(float) * simt_slot_floats(dk, dv), kAlign);
+    p.tc = gdn_use_tc(dt, dk, dv);
+    p.gate_bytes = p.tc ? 0 : round_up(sizeof(float) * (size_t)p.f.Ttot * H * dk, kAlign);
+    p.slot_bytes = p.tc ? gdn::kSlot : round_up(sizeof(float) * simt_slot_floats(dk, dv), kAlign);
     p.total = sizeof(WsHeader) + p.f.off_bytes + p.gate_bytes + (size_t)p.f.max_chunks * H * p.slot_bytes;
     return KDA_OK;
 }
@@ -84,6 +89,11 @@ extern "C" kda_status kda_gdn_chunk_fwd(const void* q, const void* k, const void
     float* gate = (float*)(ws + sizeof(WsHeader) + p.f.off_bytes);
     float* slots = (float*)((char*)gate + p.gate_bytes);
     cudaError_t e = cudaSuccess;
+    if (p.tc) {
+        e = gdn::launch_fwd(q, k, v, log_alpha, beta, S0, S_final, out, hdr, off, cu_seqlens, p.f.Tseq, p.f.N, H, Hk,
+                            p.f.max_chunks, p.f.Ttot, (uint8_t*)slots, stream);
+        return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    }
     if (p.f.Ttot > 0) e = launch_gdn_spread_gate(log_alpha, gate, p.f.Ttot * H, dk, stream);
     if (e == cudaSuccess)
         e = dt == KDA_BF16 ? launch_simt_prefill<__nv_bfloat16>(q, k, v, gate, beta, S0, S_final, out, hdr, off,
