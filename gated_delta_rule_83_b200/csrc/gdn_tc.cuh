@@ -1,15 +1,16 @@
 // gdn_tc.cuh -- tensor-core (tcgen05 / TMEM) kernels of the scalar-gate delta rule, bf16, dk = dv = 128.
 //
 // Chunk form, 64 tokens a chunk, g_i = sum_{m <= i} log alpha_m inside the chunk (log2 units), C = 64:
-//     A_ij = beta_i 2^(g_i - g_j) k_i.k_j  (j < i)      X = (I + A)^-1
-//     P_ij =        2^(g_i - g_j) q_i.k_j  (j <= i)
-//     R_i = beta_i (v_i - 2^g_i S^T k_i)    U = X R      o_i = 2^g_i S^T q_i + (P U)_i
+//     A_ij = beta_i 2^(g_i - g_j) k_i.k_j  (j < i)      X = (I + A)^-1 diag(beta)
+//     P_ij =        2^(g_i - g_j) q_i.k_j  (j <= i)     Y = P X
+//     R_i = v_i - 2^g_i S^T k_i     U = X R      o_i = 2^g_i S^T q_i + (Y R)_i
 //     S <- 2^g_C S + sum_j 2^(g_C - g_j) k_j u_j^T
+// Y makes the output a product of what enters U as well, so that U is no operand of it.
 // Because the gate is one scalar a token it never enters a bf16 operand: k, q and v go to the tensor core
 // as they came and the decays are applied in fp32 to its results, where every factor is <= 1 for
 // log alpha <= 0.  No rescaling by a reference point is needed.
 //
-// Precision.  X, P, R, U and S are fp32; as tensor-core operands each is the sum of two bf16 parts
+// Precision.  X, P, Y, R, U and S are fp32; as tensor-core operands each is the sum of two bf16 parts
 // (hi + lo, 16 significant bits) and a product takes hi.hi + hi.lo + lo.hi, one pass less where the
 // other operand is an input.  Measured against 64 bits the states are off by 4..7e-6 where single bf16
 // operands give 3e-3.
@@ -58,18 +59,49 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v)
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-// (a, b) as two packed bf16 pairs, hi + lo
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo)
+// pairs of fp32 values in one 64-bit register, for the two-wide FMA
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b)
 {
-    hi = pack_bf16(a, b);
-    lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
+__device__ __forceinline__ void unpair(f32x2 p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, 0xbf800000bf800000ull, a); }
+// four consecutive floats of shared memory as two pairs
+__device__ __forceinline__ void lds_pairs(uint32_t addr, f32x2& a, f32x2& b)
+{
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+}
+// a pair as two packed bf16 pairs, hi + lo
+__device__ __forceinline__ void split2(f32x2 p, uint32_t& hi, uint32_t& lo)
+{
+    float a, b;
+    unpair(p, a, b);
+    hi = pack_bf16(a, b);
+    unpair(sub2(p, pair(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u))), a, b);
+    lo = pack_bf16(a, b);
+}
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) { split2(pair(a, b), hi, lo); }
 // 32 values -> 16 + 16 columns of an A operand
-__device__ __forceinline__ void tmem_put_split32(uint32_t taddr, const float* x)
+__device__ __forceinline__ void tmem_put_split32(uint32_t taddr, const f32x2* x)
 {
     uint32_t hi[16], lo[16];
 #pragma unroll
-    for (int m = 0; m < 16; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
+    for (int m = 0; m < 16; ++m) split2(x[m], hi[m], lo[m]);
     tmem_st16u(taddr, hi);
     tmem_st16u(taddr + 16, lo);
 }
@@ -79,6 +111,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* x)
     tmem_ld16(taddr + 16, x + 16);
     tmem_wait_ld();
 }
+template <int REGS> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
+template <int REGS> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
 // a whole warp waits; the answer is the same in every lane
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort)
 {
@@ -93,21 +127,26 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar)
 }
 
 // ---- workspace slot of one (chunk, head) ---------------------------------------------------------------
-// X and P as hi and lo 64 x 64 SW128 images, then fp32 rows of 64: 2^g, 2^(g_C - g), beta.
-constexpr uint32_t kXhi = 0, kXlo = 8192, kPhi = 16384, kPlo = 24576, kScal = 32768;
-constexpr uint32_t kSlot = kScal + 768;
-constexpr int kGam = 0, kW = 64, kBeta = 128;  // float offsets in the scalar rows
+// 64 x 64 SW128 images, X above Y so that one MMA can run over both: X hi, Y hi, X lo, Y lo; then fp32 rows
+// of 64: 2^g, 2^(g_C - g), beta, -2^g.
+constexpr uint32_t kYofX = 8192, kLo = 16384, kScal = 32768;
+constexpr uint32_t kSlot = kScal + 1024;
+constexpr int kGam = 0, kW = 64, kBeta = 128, kNgam = 192;  // float offsets in the scalar rows
+// The backward also takes P and (I + A)^-1: hi and lo of each.
+constexpr uint32_t kBwdP = 0, kBwdX = 16384, kBwdSlot = 32768;
 
 // ----------------------------------------------------------------------------------------------------
 // Per-chunk kernel: X, P and the scalar rows of each (chunk, head).
 //
 // One CTA of 256 threads a unit.  [k; q] k^T is one M = 128, N = 64 batch; its epilogue masks and decays
-// the 128 x 64 result.  X comes from recursive doubling over 16 x 16 blocks in fp32 on CUDA cores: the
-// product form's powers of A would lose the small entries, and the split images need X to 16 bits.
-// Bound by the latency of that dependent chain, so CTAs are kept small (60 KB) to run three an SM.
+// the 128 x 64 result.  The inverse comes from recursive doubling over 16 x 16 blocks in fp32 on CUDA
+// cores: the product form's powers of A would lose the small entries, and the split images need X to 16
+// bits.  Y is a split M = 64 product.  Bound by the latency of that dependent chain, so CTAs are kept
+// small (75 KB) to run three an SM.
 // ----------------------------------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
-constexpr uint32_t kPrepA = 32768;                      // A / X fp32 [64][68]
+constexpr uint32_t kPrepP = kSlot;                      // P hi, lo; the slot takes the [k; q] tile's place
+constexpr uint32_t kPrepA = kPrepP + 16384;             // A / X fp32 [64][68]
 constexpr uint32_t kPrepY = kPrepA + 64 * kAS * 4;      // scratch [32][36]
 constexpr uint32_t kPrepMisc = kPrepY + 32 * 36 * 4;    // g, beta, barriers
 constexpr uint32_t kPrepSmem = kPrepMisc + 1024 + 1024;
@@ -228,11 +267,12 @@ __device__ __forceinline__ void store_split8(uint8_t* hi, uint8_t* lo, uint32_t 
     *reinterpret_cast<uint4*>(lo + off) = l;
 }
 
+template <bool BWD>
 __global__ void __launch_bounds__(kPrepThreads)
 gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const float* __restrict__ la, const float* __restrict__ beta, const WsHeader* __restrict__ hdr,
                 const int* __restrict__ off, const int32_t* __restrict__ cu, int Tseq, int N, int H, int G,
-                uint8_t* __restrict__ slots)
+                uint8_t* __restrict__ slots, uint8_t* __restrict__ bslots)
 {
     extern __shared__ uint8_t smem_raw[];
     if (hdr->bad) return;
@@ -310,12 +350,11 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         } else {
 #pragma unroll
             for (int m = 0; m < 4; ++m)
-                store_split8(img + kPhi, img + kPlo, sw128_chunk_off(i, (col0 >> 3) + m, 64), x + 8 * m);
+                store_split8(sm + kPrepP, sm + kPrepP + 8192, sw128_chunk_off(i, (col0 >> 3) + m, 64), x + 8 * m);
         }
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 2) tmem_dealloc(tmem, 64);
     invert_unit_lower(sA, sY);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -323,22 +362,61 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         float x[8];
         *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(sA + r * kAS + 8 * ch);
         *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(sA + r * kAS + 8 * ch + 4);
-        store_split8(img + kXhi, img + kXlo, sw128_chunk_off(r, ch, 64), x);
+        if (BWD) {
+            uint8_t* bx = bslots + (size_t)blockIdx.x * kBwdSlot + kBwdX;
+            store_split8(bx, bx + 8192, sw128_chunk_off(r, ch, 64), x);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] *= s_b[8 * ch + c];
+        store_split8(img, img + kLo, sw128_chunk_off(r, ch, 64), x);
     }
-    uint8_t* slot = slots + (size_t)blockIdx.x * kSlot;
     if (tid < 64) {
-        float* sc = reinterpret_cast<float*>(slot + kScal);
-        sc[kGam + tid] = ex2_approx(s_g[tid]);
+        float* sc = reinterpret_cast<float*>(img + kScal);
+        const float gam = ex2_approx(s_g[tid]);
+        sc[kGam + tid] = gam;
         sc[kW + tid] = ex2_approx(s_g[63] - s_g[tid]);
         sc[kBeta + tid] = s_b[tid];
+        sc[kNgam + tid] = -gam;
     }
     fence_proxy_async();
+    fence_before_sync();
     __syncthreads();
-    if (tid == 0 && ok) {
-        bulk_s2g(slot, sb, kScal);
+    if (warp == 0) {
+        fence_after_sync();
+        if (elect_one()) {  // Y = P X
+            const uint64_t dp = desc_kmajor(sb + kPrepP, 64, 0), dx = desc_mnmajor(sb, 64, 0);
+            const uint32_t id = idesc_bf16(64, 64, false, true);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t a = dp + (uint64_t)((kk * 32) >> 4), b = dx + (uint64_t)((kk * 2048) >> 4);
+                mma_bf16(tmem, a, b, id, kk > 0);
+                mma_bf16(tmem, a + (8192 >> 4), b, id, 1);
+                mma_bf16(tmem, a, b + (kLo >> 4), id, 1);
+            }
+            mma_commit(bar_mma);
+            if (BWD) bulk_s2g(bslots + (size_t)blockIdx.x * kBwdSlot + kBwdP, sb + kPrepP, 16384);
+        }
+        __syncwarp();
+    }
+    ok = ok && mbar_wait(bar_mma, 1);
+    fence_after_sync();
+    {   // M = 64: row 16 (warp % 4) + lane % 16; the upper half-warp is 32 columns further
+        float x[16];
+        tmem_ld16_pair<32>(tmem + ((uint32_t)(32 * wq) << 16) + 16 * (warp >> 2), x);
+        tmem_wait_ld();
+        const int r = 16 * wq + (lane & 15), ch = 4 * (lane >> 4) + 2 * (warp >> 2);
+        store_split8(img + kYofX, img + kYofX + kLo, sw128_chunk_off(r, ch, 64), x);
+        store_split8(img + kYofX, img + kYofX + kLo, sw128_chunk_off(r, ch + 1, 64), x + 8);
+    }
+    fence_proxy_async();
+    fence_before_sync();
+    ok = __syncthreads_and(ok);
+    if (warp == 0 && elect_one()) {
+        if (ok) bulk_s2g(slots + (size_t)blockIdx.x * kSlot, sb, kSlot);
         bulk_commit();
         bulk_wait_all();
     }
+    if (warp == 2) tmem_dealloc(tmem, 64);
 }
 
 // ----------------------------------------------------------------------------------------------------
@@ -346,37 +424,56 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 //
 // The state is kept transposed, row = value column: every operand the chain itself produces (S, R, U)
 // then is an A operand in TMEM that a thread writes from its own registers, and every input (k, q, X, P)
-// is a B operand in shared memory as it was loaded.  Thread (warpgroup w, lane d) owns value column d:
-// state channels 64 w .. 64 w + 63 and tokens 32 w .. 32 w + 31.
+// is a B operand in shared memory as it was loaded.  Compute thread (warpgroup w, lane d) owns value
+// column d: state channels 64 w .. 64 w + 63 and tokens 32 w .. 32 w + 31.
 // Per chunk, M = 128:
-//     D1 = S^T k^T     (N = 64, 16 MMAs)           R = beta (v - 2^g D1)
-//     U  = R X^T       (N = 64, 9 MMAs + 3 narrow) U' = 2^(g_C - g) U
-//     D3 = U' k        (N = 128, 8 MMAs)           S <- 2^g_C S + D3
-//     Dq = S^T q^T (16), Po = U P^T (12)           o = 2^g Dq + Po, one chunk behind, off the chain
-// TMEM columns: 0 D1 -> R -> U', 64 Dq, 128 U (accumulator, then operand), 192 Po, 256 S operand -> D3.
-// Bound by the tensor pipe (about 2100 cycles a chunk) and three MMA round trips.
+//     D1 = S^T k^T          (N = 64, 16 MMAs)        R' = -2^g D1
+//     U  = v^T X^T + R' X^T (8 with Y's, 18 narrow)  U' = 2^(g_C - g) U
+//     D3 = U' k             (N = 128, 8 MMAs)        S <- 2^g_C S + D3
+//     Dq = S^T q^T (16), Po = R' Y^T + v^T Y^T (20)  o = 2^g Dq + Po by four warps of their own
+// X and Y are lower triangular, so tokens 32..63 are no operand of outputs 0..31.  The two warpgroups run
+// staggered: each has its own barriers, and the MMAs a warpgroup waits for are committed apart from the
+// other's, so that one's conversions run under the other's MMAs.  v enters as an operand, never through
+// registers.  What no thread waits for fills the tensor pipe's gaps: Dq under the making of R', R' Y^T under
+// that of U', v^T Y^T and the next chunk's v^T X^T under the state's update.
+// TMEM columns: 0 D1 -> R', 64 Dq, 128 U, 192 Po, 256 S operand -> D3, 384 U'.
 // ----------------------------------------------------------------------------------------------------
-constexpr int kFThreads = 320;  // 8 compute warps, an MMA warp, a copy warp
-constexpr uint32_t kFK = 0, kFV = 16384, kFQ = 32768, kFSlot = 49152;
-constexpr uint32_t kFStage = kFSlot + 33792;  // the slot, padded to 1 KB
-constexpr uint32_t kFMisc = 2 * kFStage;
-constexpr uint32_t kFSmem = kFMisc + 256 + 1024;
+constexpr int kChainOut = 0;     // the prefill: writes out and S_final
+constexpr int kChainStates = 1;  // the backward's recompute: writes each chunk's start state and U
 
-// token rows L .. 63 of a 64 x 128 SW128 tile set to zero (256 threads)
-__device__ __forceinline__ void zero_tail_rows(uint8_t* tile, int L)
+constexpr uint32_t kTmD1 = 0, kTmDq = 64, kTmU = 128, kTmPo = 192, kTmS = 256, kTmUw = 384;
+
+template <int MODE> struct Chain {
+    // 8 compute warps, [4 output warps], MMA, copies [, 2 idle: registers are shared out by warpgroup]
+    static constexpr int kThreads = MODE == kChainOut ? 512 : 320;
+    static constexpr int kMmaWarp = MODE == kChainOut ? 12 : 8;
+    static constexpr uint32_t K = 0, V = 16384, Slot = 32768;  // (kChainStates: X hi, X lo, scalars)
+    static constexpr uint32_t Scal = Slot + (MODE == kChainOut ? kScal : 16384u);
+    static constexpr uint32_t Q = Scal + 1024;                 // kChainOut
+    static constexpr uint32_t Stage = MODE == kChainOut ? Q + 16384 : Scal + 1024;
+    static constexpr uint32_t XLo = MODE == kChainOut ? kLo : 8192u;  // from a hi image to its lo one
+    static constexpr uint32_t Img = 2 * Stage;  // kChainStates: S hi, lo (32 KB each), U hi, lo (16 KB each)
+    static constexpr uint32_t Misc = Img + (MODE == kChainStates ? 98304u : 0u);
+    static constexpr uint32_t Smem = Misc + 512 + 2048 + 1024;
+};
+
+// token rows L .. 63 of one 64-channel atom column set to zero by a warpgroup
+__device__ __forceinline__ void zero_tail_rows(uint8_t* atom, int L)
 {
-    for (int e = threadIdx.x; e < (64 - L) * 16; e += 256) {
-        const int r = L + (e >> 4), ch = e & 15;
-        *reinterpret_cast<uint4*>(tile + sw128_chunk_off(r, ch, 64)) = make_uint4(0, 0, 0, 0);
-    }
+    for (int e = threadIdx.x & 127; e < (64 - L) * 8; e += 128)
+        *reinterpret_cast<uint4*>(atom + (L + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
 
-__global__ void __launch_bounds__(kFThreads, 1)
+template <int MODE>
+__global__ void __launch_bounds__(Chain<MODE>::kThreads, 1)
 gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const float* S0, float* S_final,
                  __nv_bfloat16* __restrict__ out, const WsHeader* __restrict__ hdr, const int* __restrict__ off,
-                 const int32_t* __restrict__ cu, int Tseq, int N, int H, int G, const uint8_t* __restrict__ slots)
+                 const int32_t* __restrict__ cu, int Tseq, int N, int H, int G, const uint8_t* __restrict__ slots,
+                 uint8_t* __restrict__ images)
 {
+    using C = Chain<MODE>;
+    constexpr bool kOut = MODE == kChainOut;
     extern __shared__ uint8_t smem_raw[];
     if (hdr->bad) return;
     const int rank = blockIdx.x / H, h = blockIdx.x - rank * H, n = off[N + 1 + rank];
@@ -385,24 +482,32 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     seq_bounds(n, cu, Tseq, s0, s1);
     uint8_t* sm = align1024(smem_raw);
     const uint32_t sb = smem_u32(sm);
-    const uint32_t bars = sb + kFMisc;
-    const uint32_t bar_full = bars, bar_empty = bars + 16, bar_k = bars + 32, bar_u = bars + 40, bar_d = bars + 48,
-                   bar_o = bars + 56, bar_s = bars + 64, bar_r = bars + 72, bar_u2 = bars + 80;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + kFMisc + 96);
-    volatile int* s_abort = reinterpret_cast<volatile int*>(sm + kFMisc + 100);
+    const uint32_t bars = sb + C::Misc;
+    const uint32_t bar_full = bars, bar_empty = bars + 16, bar_k = bars + 32, bar_u = bars + 48, bar_d = bars + 64,
+                   bar_s = bars + 80, bar_r = bars + 96, bar_w = bars + 112, bar_o = bars + 128, bar_q = bars + 136,
+                   bar_z = bars + 144;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + C::Misc + 160);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(sm + C::Misc + 164);
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, 8);
+            mbar_init(bar_empty + 8 * s, kOut ? 13 : 9);  // readers' warps and the last MMAs
+            mbar_init(bar_k + 8 * s, 1);
+            mbar_init(bar_u + 8 * s, 1);
+            mbar_init(bar_d + 8 * s, 1);
+            mbar_init(bar_s + 8 * s, 4);
+            mbar_init(bar_r + 8 * s, 4);
+            mbar_init(bar_w + 8 * s, 4);
         }
-        mbar_init(bar_k, 1); mbar_init(bar_u, 1); mbar_init(bar_d, 1); mbar_init(bar_o, 1);
-        mbar_init(bar_s, 8); mbar_init(bar_r, 8); mbar_init(bar_u2, 8);
+        mbar_init(bar_o, 1);
+        mbar_init(bar_q, 4);
+        mbar_init(bar_z, 8);
         mbar_fence_init();
         *s_abort = 0;
     }
-    if (warp == 8) {
+    if (warp == C::kMmaWarp) {
         tmem_alloc(smem_u32(s_tmem), 512);
         tmem_relinquish();
     }
@@ -412,229 +517,309 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t tmem = uniform(*s_tmem);
     bool ok = true;
 
-    if (warp == 9) {  // loads, two stages
+    // 512 threads x 128 registers at launch = 2 x 128 x 176 + 128 x 96 + 128 x 64
+    if (kOut && warp >= 12) regs_dec<64>();
+    if (warp == C::kMmaWarp + 1) {  // loads, two stages
         for (int it = 0; it < nch && ok; ++it) {
             const int s = it & 1;
             if (it >= 2) ok = warp_wait(bar_empty + 8 * s, (uint32_t)((it >> 1) - 1) & 1u, s_abort);
             if (ok && elect_one()) {
-                const uint32_t st = sb + s * kFStage, f = bar_full + 8 * s;
+                const uint32_t st = sb + s * C::Stage, f = bar_full + 8 * s;
                 const int t = (int)(s0 + 64LL * it);
-                mbar_arrive_expect_tx(f, 49152 + kSlot);
+                const uint8_t* slot = slots + ((size_t)(jb + it) * H + h) * kSlot;
+                mbar_arrive_expect_tx(f, kOut ? 49152 + kSlot : 32768 + 16384 + 1024);
                 for (int a = 0; a < 2; ++a) {
-                    tma_load_3d(st + kFK + 8192 * a, &tm_k, 64 * a, h / G, t, f);
-                    tma_load_3d(st + kFQ + 8192 * a, &tm_q, 64 * a, h / G, t, f);
-                    tma_load_3d(st + kFV + 8192 * a, &tm_v, 64 * a, h, t, f);
+                    tma_load_3d(st + C::K + 8192 * a, &tm_k, 64 * a, h / G, t, f);
+                    if (kOut) tma_load_3d(st + C::Q + 8192 * a, &tm_q, 64 * a, h / G, t, f);
+                    tma_load_3d(st + C::V + 8192 * a, &tm_v, 64 * a, h, t, f);
                 }
-                bulk_g2s(st + kFSlot, slots + ((size_t)(jb + it) * H + h) * kSlot, kSlot, f);
+                if (kOut) {
+                    bulk_g2s(st + C::Slot, slot, kSlot, f);
+                } else {
+                    bulk_g2s(st + C::Slot, slot, 8192, f);
+                    bulk_g2s(st + C::Slot + 8192, slot + kLo, 8192, f);
+                    bulk_g2s(st + C::Scal, slot + kScal, 1024, f);
+                }
             }
             __syncwarp();
         }
         for (int it = nch > 2 ? nch - 2 : 0; it < nch; ++it)  // no copy outlives the CTA, whatever gave up
             if (!ok) (void)mbar_wait(bar_full + 8 * (it & 1), (uint32_t)(it >> 1) & 1u);
-    } else if (warp == 8) {  // MMA issue
-        const uint32_t id64 = idesc_bf16(128, 64, false, false), id32 = idesc_bf16(128, 32, false, false),
-                       idd = idesc_bf16(128, 128, false, true);
+    } else if (warp == C::kMmaWarp) {
+        const uint32_t id128m = idesc_bf16(128, 128, false, true), id64 = idesc_bf16(128, 64, false, false),
+                       id32 = idesc_bf16(128, 32, false, false), id64m = idesc_bf16(128, 64, false, true),
+                       idv = idesc_bf16(128, 64, true, false);
+        auto v_times = [&](uint32_t d, uint64_t dv, uint64_t b, uint32_t first) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t a = dv + (uint64_t)((kk * 2048) >> 4), bb = b + (uint64_t)((kk * 32) >> 4);
+                mma_bf16(d, a, bb, idv, kk > 0 || !first);
+                mma_bf16(d, a, bb + (C::XLo >> 4), idv, 1);
+            }
+        };
+        // U = v^T X^T of chunk `it`, into the accumulator that the chunk before has been read from
+        auto issue_v = [&](int it) {
+            const uint32_t st = sb + (it & 1) * C::Stage;
+            ok = ok && warp_wait(bar_full + 8 * (it & 1), (uint32_t)(it >> 1) & 1u, s_abort);
+            ok = ok && warp_wait(bar_z, (uint32_t)it & 1u, s_abort);
+            fence_after_sync();
+            if (ok && elect_one()) v_times(tmem + kTmU, desc_mnmajor(st + C::V, 64, 0), desc_kmajor(st + C::Slot, 64, 0), 1);
+            __syncwarp();
+        };
+        if (nch > 0) issue_v(0);
         for (int it = 0; it < nch; ++it) {
             const int s = it & 1;
-            const uint32_t st = sb + s * kFStage, par = (uint32_t)it & 1u;
-            const uint64_t dk = desc_kmajor(st + kFK, 64, 0), dq = desc_kmajor(st + kFQ, 64, 0),
-                           dkm = desc_mnmajor(st + kFK, 64, 0), dX = desc_kmajor(st + kFSlot, 64, 0);
-            ok = ok && warp_wait(bar_full + 8 * s, (uint32_t)(it >> 1) & 1u, s_abort);
-            ok = ok && warp_wait(bar_s, par, s_abort);
-            fence_after_sync();
-            if (ok && elect_one()) {  // D1 = (S_hi + S_lo) k^T
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t a = tmem + 256 + 64 * (kk >> 2) + 8 * (kk & 3);
-                    const uint64_t b = dk + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
-                    mma_ts(tmem, a, b, id64, kk > 0);
-                    mma_ts(tmem, a + 32, b, id64, 1);
-                }
-                mma_commit(bar_k);
-            }
-            __syncwarp();
-            if (it > 0) ok = ok && warp_wait(bar_empty + 8 * (s ^ 1), (uint32_t)((it - 1) >> 1) & 1u, s_abort);
-            fence_after_sync();
-            if (ok && elect_one()) {  // Dq; the last chunk's has been read
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t a = tmem + 256 + 64 * (kk >> 2) + 8 * (kk & 3);
-                    const uint64_t b = dq + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
-                    mma_ts(tmem + 64, a, b, id64, kk > 0);
-                    mma_ts(tmem + 64, a + 32, b, id64, 1);
-                }
-            }
-            __syncwarp();
-            ok = ok && warp_wait(bar_r, par, s_abort);
-            fence_after_sync();
-            if (ok && elect_one()) {  // U = R X^T; X is lower triangular: tokens 32..63 reach outputs 32..63 alone
+            const uint32_t st = sb + s * C::Stage, par = (uint32_t)it & 1u;
+            const uint64_t dk = desc_kmajor(st + C::K, 64, 0), dq = desc_kmajor(st + C::Q, 64, 0),
+                           dkm = desc_mnmajor(st + C::K, 64, 0), dX = desc_kmajor(st + C::Slot, 64, 0),
+                           dY = dX + (uint64_t)(kYofX >> 4);
+            // S operand: channels 64 a .. of warpgroup a, hi at column 64 a, lo 32 further
+            auto state_times = [&](uint32_t d, uint64_t b, int a, uint32_t id, uint32_t first) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    const uint32_t a = tmem + 32 * (kk >> 1) + 8 * (kk & 1), d = tmem + 128 + (kk >> 1) * 32;
-                    const uint64_t b = dX + (uint64_t)((kk * 32 + (kk >> 1) * 32 * 128) >> 4);
-                    const uint32_t id = kk < 2 ? id64 : id32;
-                    mma_ts(d, a, b, id, kk > 0);
-                    mma_ts(d, a + 16, b, id, 1);
-                    mma_ts(d, a, b + (kXlo >> 4), id, 1);
+                    const uint32_t x = tmem + kTmS + 64 * a + 8 * kk;
+                    const uint64_t bb = b + (uint64_t)((a * 8192 + kk * 32) >> 4);
+                    mma_ts(d, x, bb, id, kk > 0 || !first);
+                    mma_ts(d, x + 32, bb, id, 1);
                 }
-                mma_commit(bar_u);
+            };
+            // R' (two k steps of warpgroup a) times rows of a split image
+            auto r_times = [&](uint32_t d, uint64_t b, int a, uint32_t id, uint32_t first) {
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const uint32_t x = tmem + kTmD1 + 32 * a + 8 * kk;
+                    const uint64_t bb = b + (uint64_t)((a * 64 + kk * 32) >> 4);
+                    mma_ts(d, x, bb, id, kk > 0 || !first);
+                    mma_ts(d, x + 16, bb, id, 1);
+                    mma_ts(d, x, bb + (C::XLo >> 4), id, 1);
+                }
+            };
+            ok = ok && warp_wait(bar_s, par, s_abort);
+            fence_after_sync();
+            if (ok && elect_one()) state_times(tmem + kTmD1, dk, 0, id64, 1);
+            __syncwarp();
+            ok = ok && warp_wait(bar_s + 8, par, s_abort);
+            fence_after_sync();
+            if (ok && elect_one()) {
+                state_times(tmem + kTmD1, dk, 1, id32, 0);
+                mma_commit(bar_k);
+                state_times(tmem + kTmD1 + 32, dk + (uint64_t)(4096 >> 4), 1, id32, 0);
+                mma_commit(bar_k + 8);
             }
             __syncwarp();
-            ok = ok && warp_wait(bar_u2, par, s_abort);
+            if (kOut) {
+                if (it > 0) ok = ok && warp_wait(bar_q, par ^ 1u, s_abort);  // the last chunk's Dq and Po are read
+                fence_after_sync();
+                if (ok && elect_one()) {
+                    state_times(tmem + kTmDq, dq, 0, id64, 1);
+                    state_times(tmem + kTmDq, dq, 1, id64, 0);
+                }
+                __syncwarp();
+            }
+            ok = ok && warp_wait(bar_r, par, s_abort);
+            fence_after_sync();
+            if (ok && elect_one()) {
+                r_times(tmem + kTmU, dX, 0, id32, 0);
+                mma_commit(bar_u);
+                r_times(tmem + kTmU + 32, dX + (uint64_t)(4096 >> 4), 0, id32, 0);
+            }
+            __syncwarp();
+            ok = ok && warp_wait(bar_r + 8, par, s_abort);
+            fence_after_sync();
+            if (ok && elect_one()) {
+                r_times(tmem + kTmU + 32, dX + (uint64_t)(4096 >> 4), 1, id32, 0);
+                mma_commit(bar_u + 8);
+                if (kOut) {
+                    r_times(tmem + kTmPo, dY, 0, id64, 1);
+                    r_times(tmem + kTmPo + 32, dY + (uint64_t)(4096 >> 4), 1, id32, 0);
+                }
+            }
+            __syncwarp();
+            ok = ok && warp_wait(bar_w, par, s_abort);
+            fence_after_sync();
+            if (ok && elect_one()) {  // D3 over the state operand, which D1 and Dq have consumed
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const uint32_t x = tmem + kTmUw + 8 * kk;
+                    const uint64_t b = dkm + (uint64_t)((kk * 2048) >> 4);
+                    mma_ts(tmem + kTmS, x, b, id128m, kk > 0);
+                    mma_ts(tmem + kTmS, x + 16, b, id128m, 1);
+                }
+            }
+            __syncwarp();
+            ok = ok && warp_wait(bar_w + 8, par, s_abort);
             fence_after_sync();
             if (ok && elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {  // D3 = U' k, over the state operand
-                    const uint32_t a = tmem + 32 * (kk >> 1) + 8 * (kk & 1);
-                    const uint64_t b = dkm + (uint64_t)((kk * 2048) >> 4);
-                    mma_ts(tmem + 256, a, b, idd, kk > 0);
-                    mma_ts(tmem + 256, a + 16, b, idd, 1);
-                }
-                mma_commit(bar_d);
+                for (int a = 0; a < 2; ++a) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {  // Po = U P^T
-                    const uint32_t a = tmem + 128 + 32 * (kk >> 1) + 8 * (kk & 1), d = tmem + 192 + (kk >> 1) * 32;
-                    const uint64_t b = dX + (uint64_t)((kPhi + kk * 32 + (kk >> 1) * 32 * 128) >> 4);
-                    const uint32_t id = kk < 2 ? id64 : id32;
-                    mma_ts(d, a, b, id, kk > 0);
-                    mma_ts(d, a + 16, b, id, 1);
-                    mma_ts(d, a, b + ((kPlo - kPhi) >> 4), id, 1);
+                    for (int kk = 0; kk < 2; ++kk) {
+                        const uint32_t x = tmem + kTmUw + 32 + 8 * kk;
+                        const uint64_t b = dkm + (uint64_t)(((2 + kk) * 2048 + a * 8192) >> 4);
+                        mma_ts(tmem + kTmS + 64 * a, x, b, id64m, 1);
+                        mma_ts(tmem + kTmS + 64 * a, x + 16, b, id64m, 1);
+                    }
+                    mma_commit(bar_d + 8 * a);
                 }
-                mma_commit(bar_o);
+                if (kOut) {
+                    v_times(tmem + kTmPo, desc_mnmajor(st + C::V, 64, 0), dY, 0);
+                    mma_commit(bar_o);
+                }
+                mma_commit(bar_empty + 8 * s);
             }
             __syncwarp();
+            if (it + 1 < nch) issue_v(it + 1);
         }
-        if (nch > 0) (void)(ok && warp_wait(bar_o, (uint32_t)(nch - 1) & 1u, s_abort));
+    } else if (warp >= C::kMmaWarp) {  // idle
+    } else if (kOut && warp >= 8) {  // output warps: value column d, all 64 tokens
+        const int wq = warp & 3, d = 32 * wq + lane;
+        const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
+        float* s_gam = reinterpret_cast<float*>(sm + C::Misc + 512) + wq * 64;
+        const bool odd = lane & 1;
+        regs_dec<96>();
+        for (int it = 0; it < nch; ++it) {
+            const int s = it & 1;
+            ok = ok && mbar_wait_ab(bar_full + 8 * s, (uint32_t)(it >> 1) & 1u, s_abort);
+            {   // 2^g, kept past the stage's end
+                const float* sc = reinterpret_cast<const float*>(sm + s * C::Stage + C::Scal) + kGam;
+                const float2 g2 = *reinterpret_cast<const float2*>(sc + 2 * lane);
+                __syncwarp();
+                *reinterpret_cast<float2*>(s_gam + 2 * lane) = g2;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+            }
+            ok = ok && mbar_wait_ab(bar_o, (uint32_t)it & 1u, s_abort);
+            fence_after_sync();
+            const long long t = s0 + 64LL * it;
+            const int L = (int)(s1 - t < 64 ? s1 - t : 64);
+            uint32_t z[32];  // tokens 2 m, 2 m + 1 of column d
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                float x[16], y[16];
+                tmem_ld16(tl + kTmDq + c, x);
+                tmem_ld16(tl + kTmPo + c, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int m = 0; m < 16; m += 4) {
+                    const float4 g4 = *reinterpret_cast<const float4*>(s_gam + c + m);
+                    z[(c + m) / 2] = pack_bf16(fmaf(g4.x, x[m], y[m]), fmaf(g4.y, x[m + 1], y[m + 1]));
+                    z[(c + m) / 2 + 1] = pack_bf16(fmaf(g4.z, x[m + 2], y[m + 2]), fmaf(g4.w, x[m + 3], y[m + 3]));
+                }
+            }
+            warp_arrive(bar_q);
+            // neighbours exchange: the even lane stores columns (d, d + 1) of the even token, the odd lane of the odd
+            const size_t row = (size_t)H * 128;
+            __nv_bfloat16* o = out + ((size_t)t * H + h) * 128 + (d & ~1) + (odd ? row : 0);
+#pragma unroll
+            for (int m = 0; m < 32; ++m) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, z[m], 1);
+                const uint32_t two = odd ? __byte_perm(got, z[m], 0x7632) : __byte_perm(z[m], got, 0x5410);
+                if (ok && 2 * m + (odd ? 1 : 0) < L) *reinterpret_cast<uint32_t*>(o + (size_t)(2 * m) * row) = two;
+            }
+        }
     } else {
         const int wg = warp >> 2, d = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const size_t srow = ((size_t)n * H + h) * 16384 + (size_t)wg * 64 * 128 + d;
-        float S[64];
+        if (kOut) regs_inc<176>();
+        f32x2 S[32];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) S[c] = S0 ? S0[srow + (size_t)c * 128] : 0.f;
-        auto put_state = [&]() {  // channels 64 w ..: 32 columns of hi, then 32 of lo
-            uint32_t hi[32], lo[32];
+        for (int c = 0; c < 32; ++c)
+            S[c] = S0 ? pair(S0[srow + (size_t)(2 * c) * 128], S0[srow + (size_t)(2 * c + 1) * 128]) : 0ull;
+        // the state operand of chunk `it`; its last chunk's token rows past the sequence's end hold other
+        // tokens, whose values may be anything, and are cleared before the tensor core reads them
+        auto put_state = [&](int it) {
 #pragma unroll
-            for (int m = 0; m < 32; ++m) split2(S[2 * m], S[2 * m + 1], hi[m], lo[m]);
-            tmem_st16u(tl + 256 + 64 * wg, hi);
-            tmem_st16u(tl + 256 + 64 * wg + 16, hi + 16);
-            tmem_st16u(tl + 256 + 64 * wg + 32, lo);
-            tmem_st16u(tl + 256 + 64 * wg + 48, lo + 16);
+            for (int b = 0; b < 2; ++b) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int m = 0; m < 16; ++m) split2(S[16 * b + m], hi[m], lo[m]);
+                tmem_st16u(tl + kTmS + 64 * wg + 16 * b, hi);
+                tmem_st16u(tl + kTmS + 64 * wg + 32 + 16 * b, lo);
+            }
             tmem_wait_st();
+            if (it < nch) warp_arrive(bar_s + 8 * wg);
         };
-        put_state();
-        // o of chunk `it`: tokens 32 w .. 32 w + 31 of value column d
-        auto write_out = [&](int it) {
-            const int s = it & 1;
-            const float* sc = reinterpret_cast<const float*>(sm + s * kFStage + kFSlot + kScal);
-            ok = ok && mbar_wait_ab(bar_o, (uint32_t)it & 1u, s_abort);
-            fence_after_sync();
-            float x[32], y[32];
-            tmem_ld16(tl + 64 + 32 * wg, x);
-            tmem_ld16(tl + 64 + 32 * wg + 16, x + 16);
-            tmem_ld16(tl + 192 + 32 * wg, y);
-            tmem_ld16(tl + 192 + 32 * wg + 16, y + 16);
-            tmem_wait_ld();
-#pragma unroll
-            for (int m = 0; m < 32; m += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(sc + kGam + 32 * wg + m);
-                x[m] = fmaf(g4.x, x[m], y[m]);
-                x[m + 1] = fmaf(g4.y, x[m + 1], y[m + 1]);
-                x[m + 2] = fmaf(g4.z, x[m + 2], y[m + 2]);
-                x[m + 3] = fmaf(g4.w, x[m + 3], y[m + 3]);
-            }
-            warp_arrive(bar_empty + 8 * s);  // stage, Dq and Po are free
-            // neighbours exchange halves: the even lane stores columns (d, d + 1) of the even token
-            const long long t = s0 + 64LL * it + 32 * wg;
-            const int Lw = (int)(s1 - t < 32 ? s1 - t : 32);
-            __nv_bfloat16* o = out + ((size_t)t * H + h) * 128 + (d & ~1);
-            const bool odd = lane & 1;
-#pragma unroll
-            for (int m = 0; m < 32; m += 2) {
-                const float give = odd ? x[m] : x[m + 1], keep = odd ? x[m + 1] : x[m];
-                const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-                const int tok = m + (odd ? 1 : 0);
-                if (ok && tok < Lw)
-                    *reinterpret_cast<uint32_t*>(o + (size_t)tok * H * 128) = odd ? pack_bf16(got, keep) : pack_bf16(keep, got);
-            }
-        };
-        for (int it = 0; it < nch; ++it) {
-            const int s = it & 1;
-            const uint32_t par = (uint32_t)it & 1u;
-            uint8_t* st = sm + s * kFStage;
-            const float* sc = reinterpret_cast<const float*>(st + kFSlot + kScal);
-            const int L = (int)(s1 - (s0 + 64LL * it) < 64 ? s1 - (s0 + 64LL * it) : 64);
-            ok = ok && mbar_wait_ab(bar_full + 8 * s, (uint32_t)(it >> 1) & 1u, s_abort);
-            if (L < 64) {  // rows past the sequence's end: another sequence's tokens
+        // The last chunk's token rows past the sequence's end hold other tokens, whose values may be anything:
+        // cleared before the tensor core reads them.
+        auto clear_tail = [&](int it) {
+            const long long left = s1 - (s0 + 64LL * it);
+            if (left < 64) {
+                uint8_t* st = sm + (it & 1) * C::Stage;
+                ok = ok && mbar_wait_ab(bar_full + 8 * (it & 1), (uint32_t)(it >> 1) & 1u, s_abort);
                 if (ok) {
-                    zero_tail_rows(st + kFK, L);
-                    zero_tail_rows(st + kFQ, L);
+                    zero_tail_rows(st + C::K + 8192 * wg, (int)left);
+                    zero_tail_rows(st + C::V + 8192 * wg, (int)left);
+                    if (kOut) zero_tail_rows(st + C::Q + 8192 * wg, (int)left);
                 }
                 fence_proxy_async();
             }
-            warp_arrive(bar_s);
-            if (it > 0) write_out(it - 1);
-            float v[32];
-            {
-                const uint8_t* tv = st + kFV + (d >> 6) * 8192 + (d & 7) * 2;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_z);
+        };
+        if (nch > 0) clear_tail(0);
+        put_state(0);
+        for (int it = 0; it < nch; ++it) {
+            const int s = it & 1;
+            const uint32_t par = (uint32_t)it & 1u;
+            const uint32_t sc = sb + s * C::Stage + C::Scal;
+            ok = ok && mbar_wait_ab(bar_full + 8 * s, (uint32_t)(it >> 1) & 1u, s_abort);
+            // this warpgroup's token rows of two scalars, while D1 runs
+            f32x2 ng[16], w[16];
 #pragma unroll
-                for (int m = 0; m < 32; ++m) {
-                    const int j = 32 * wg + m;
-                    v[m] = lds_bf16(tv + j * 128 + ((((d & 63) >> 3) ^ (j & 7)) << 4));
-                }
+            for (int m = 0; m < 16; m += 2) {
+                lds_pairs(sc + 4 * (kNgam + 32 * wg + 2 * m), ng[m], ng[m + 1]);
+                lds_pairs(sc + 4 * (kW + 32 * wg + 2 * m), w[m], w[m + 1]);
             }
             float x[32];
-            ok = ok && mbar_wait_ab(bar_k, par, s_abort);
+            f32x2 y[16];
+            ok = ok && mbar_wait_ab(bar_k + 8 * wg, par, s_abort);
             fence_after_sync();
-            tmem_ld32(tl + 32 * wg, x);
+            tmem_ld32(tl + kTmD1 + 32 * wg, x);
 #pragma unroll
-            for (int m = 0; m < 32; m += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(sc + kGam + 32 * wg + m);
-                const float4 b4 = *reinterpret_cast<const float4*>(sc + kBeta + 32 * wg + m);
-                x[m] = b4.x * fmaf(-g4.x, x[m], v[m]);
-                x[m + 1] = b4.y * fmaf(-g4.y, x[m + 1], v[m + 1]);
-                x[m + 2] = b4.z * fmaf(-g4.z, x[m + 2], v[m + 2]);
-                x[m + 3] = b4.w * fmaf(-g4.w, x[m + 3], v[m + 3]);
-            }
-            if (L < 64) {
-#pragma unroll
-                for (int m = 0; m < 32; ++m) x[m] = 32 * wg + m < L ? x[m] : 0.f;
-            }
-            tmem_put_split32(tl + 32 * wg, x);
+            for (int m = 0; m < 16; ++m) y[m] = mul2(ng[m], pair(x[2 * m], x[2 * m + 1]));
+            tmem_put_split32(tl + kTmD1 + 32 * wg, y);
             tmem_wait_st();
-            warp_arrive(bar_r);
-            const float last = sc[kGam + 63];
-            ok = ok && mbar_wait_ab(bar_u, par, s_abort);
+            warp_arrive(bar_r + 8 * wg);
+            float last1;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(last1) : "r"(sc + 4 * (kGam + 63)));
+            const f32x2 last = pair(last1, last1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+            ok = ok && mbar_wait_ab(bar_u + 8 * wg, par, s_abort);
             fence_after_sync();
-            tmem_ld32(tl + 128 + 32 * wg, x);
-            tmem_put_split32(tl + 128 + 32 * wg, x);
+            tmem_ld32(tl + kTmU + 32 * wg, x);
 #pragma unroll
-            for (int m = 0; m < 32; m += 4) {
-                const float4 w4 = *reinterpret_cast<const float4*>(sc + kW + 32 * wg + m);
-                x[m] *= w4.x; x[m + 1] *= w4.y; x[m + 2] *= w4.z; x[m + 3] *= w4.w;
-            }
-            tmem_put_split32(tl + 32 * wg, x);
+            for (int m = 0; m < 16; ++m) y[m] = mul2(w[m], pair(x[2 * m], x[2 * m + 1]));
+            tmem_put_split32(tl + kTmUw + 32 * wg, y);
             tmem_wait_st();
-            warp_arrive(bar_u2);
-            ok = ok && mbar_wait_ab(bar_d, par, s_abort);
+            warp_arrive(bar_w + 8 * wg);
+            if (it + 1 < nch) clear_tail(it + 1);
+            ok = ok && mbar_wait_ab(bar_d + 8 * wg, par, s_abort);
             fence_after_sync();
+            {
+                float z[64];
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-                tmem_ld32(tl + 256 + 64 * wg + c, x);
+                for (int c = 0; c < 64; c += 16) tmem_ld16(tl + kTmS + 64 * wg + c, z + c);
+                tmem_wait_ld();
 #pragma unroll
-                for (int m = 0; m < 32; ++m) S[c + m] = fmaf(last, S[c + m], x[m]);
+                for (int m = 0; m < 32; ++m) S[m] = fma2(last, S[m], pair(z[2 * m], z[2 * m + 1]));
             }
-            put_state();
+            put_state(it + 1);
         }
-        if (nch > 0) write_out(nch - 1);
         if (S_final && ok) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) S_final[srow + (size_t)c * 128] = S[c];
+            for (int c = 0; c < 32; ++c) {
+                float a, b;
+                unpair(S[c], a, b);
+                S_final[srow + (size_t)(2 * c) * 128] = a;
+                S_final[srow + (size_t)(2 * c + 1) * 128] = b;
+            }
         }
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 inline size_t slots_bytes(long long units) { return (size_t)units * kSlot; }
@@ -643,11 +828,11 @@ inline cudaError_t launch_prep(const CUtensorMap& tq, const CUtensorMap& tk, con
                                const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq, int N, int H, int Hk,
                                long long units, uint8_t* slots, cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(gdn_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
+    const cudaError_t e = cudaFuncSetAttribute(gdn_prep_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
     if (e != cudaSuccess) return e;
     LaunchScope ls("gdn_prep", stream);
-    gdn_prep_kernel<<<(unsigned)units, kPrepThreads, kPrepSmem, stream>>>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H,
-                                                                         H / Hk, slots);
+    gdn_prep_kernel<false><<<(unsigned)units, kPrepThreads, kPrepSmem, stream>>>(tq, tk, la, beta, hdr, off, cu, Tseq, N,
+                                                                                H, H / Hk, slots, nullptr);
     return cudaGetLastError();
 }
 
@@ -667,11 +852,12 @@ inline cudaError_t launch_fwd(const void* q, const void* k, const void* v, const
         e = launch_prep(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, slots, stream);
         if (e != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(gdn_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFSmem);
+    using C = Chain<kChainOut>;
+    e = cudaFuncSetAttribute(gdn_chain_kernel<kChainOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
     if (e != cudaSuccess) return e;
     LaunchScope ls("gdn_chain", stream);
-    gdn_chain_kernel<<<(unsigned)(N * H), kFThreads, kFSmem, stream>>>(tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, hdr,
-                                                                      off, cu, Tseq, N, H, H / Hk, slots);
+    gdn_chain_kernel<kChainOut><<<(unsigned)(N * H), C::kThreads, C::Smem, stream>>>(
+        tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, hdr, off, cu, Tseq, N, H, H / Hk, slots, nullptr);
     return cudaGetLastError();
 }
 
