@@ -29,6 +29,7 @@ kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, i
 
 struct GdnBwdPlan {
     BwdPlan b;
+    bool tc;
     size_t gate_bytes, total;
 };
 
@@ -37,6 +38,13 @@ kda_status make_gdn_bwd_plan(int B, int T, int H, int Hk, int dk, int dv, bool v
 {
     const kda_status st = make_bwd_plan(B, T, H, Hk, 0u, dk, dv, varlen, num_seqs, dt, p.b);
     if (st != KDA_OK) return st;
+    p.tc = gdn_use_tc(dt, dk, dv);
+    if (p.tc) {
+        p.gate_bytes = 0;
+        p.total = sizeof(WsHeader) + p.b.f.off_bytes +
+                  gdn::bwd_layout((long long)p.b.f.max_chunks * H, p.b.f.Ttot, H, Hk != H).total;
+        return KDA_OK;
+    }
     p.gate_bytes = round_up(sizeof(float) * (size_t)p.b.f.Ttot * H * dk, kAlign);
     p.total = round_up(p.b.total_bytes, kAlign) + 2 * p.gate_bytes;
     return KDA_OK;
@@ -137,6 +145,21 @@ extern "C" kda_status kda_gdn_chunk_bwd(const void* q, const void* k, const void
         ((uintptr_t)cu_seqlens & 3u))
         return KDA_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace % kAlign) || workspace_bytes < p.total) return KDA_ERR_WORKSPACE;
+    if (p.tc) {
+        const Plan& f = p.b.f;
+        char* ws = (char*)workspace;
+        WsHeader* hdr = (WsHeader*)ws;
+        int* off = (int*)(ws + sizeof(WsHeader));
+        {
+            LaunchScope ls("chunk_table", stream);
+            chunk_table_kernel<<<1, kTableThreads, 0, stream>>>(cu_seqlens, f.N, f.Tseq, f.Ttot, hdr, off, off + f.N + 1);
+            if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
+        }
+        const cudaError_t e = gdn::launch_bwd(q, k, v, log_alpha, beta, S0, dout, dS_final, dq, dk_out, dv_out, dlog_alpha,
+                                              dbeta, dS0, hdr, off, cu_seqlens, f.Tseq, f.N, H, Hk, f.max_chunks, Ttot,
+                                              (uint8_t*)(ws + sizeof(WsHeader) + f.off_bytes), stream);
+        return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    }
     float* gate = (float*)((char*)workspace + round_up(p.b.total_bytes, kAlign));
     float* dgate = (float*)((char*)gate + p.gate_bytes);
     if (Ttot > 0 && launch_gdn_spread_gate(log_alpha, gate, Ttot * H, dk, stream) != cudaSuccess) return KDA_ERR_CUDA;

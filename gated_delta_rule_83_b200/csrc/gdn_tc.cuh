@@ -132,8 +132,13 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar)
 constexpr uint32_t kYofX = 8192, kLo = 16384, kScal = 32768;
 constexpr uint32_t kSlot = kScal + 1024;
 constexpr int kGam = 0, kW = 64, kBeta = 128, kNgam = 192;  // float offsets in the scalar rows
-// The backward also takes P and (I + A)^-1: hi and lo of each.
-constexpr uint32_t kBwdP = 0, kBwdX = 16384, kBwdSlot = 32768;
+// The backward also takes P, (I + A)^-1 and 2^g q (64 x 128): hi and lo of each.
+constexpr uint32_t kBwdP = 0, kBwdX = 16384, kBwdQ = 32768, kBwdSlot = 65536;
+// ... and what the chains hand to the gradient kernel, per (chunk, head), hi and lo: the state before the chunk
+// and its cotangent after it (128 value columns x 128 channels), U and dR (128 value columns x 64 tokens).
+// Row d of these unswizzled images is value column d, 16-byte blocks of 8 columns 2 KB apart: a thread that
+// owns row d stores whole blocks and a warp's store is one run of 512 bytes.
+constexpr uint32_t kImgS = 0, kImgDs = 65536, kImgU = 131072, kImgDr = 163840, kImages = 196608;
 
 // ----------------------------------------------------------------------------------------------------
 // Per-chunk kernel: X, P and the scalar rows of each (chunk, head).
@@ -355,6 +360,19 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
     fence_before_sync();
     __syncthreads();
+    if (BWD) {  // 2^g q, before the images take the tile's place
+        uint8_t* bq = bslots + (size_t)blockIdx.x * kBwdSlot + kBwdQ;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int e = tid + kPrepThreads * m, r = e >> 4, ch = e & 15;
+            const float gam = ex2_approx(s_g[r]);
+            float x[8];
+            unpack8(*reinterpret_cast<const uint4*>(sm + sw128_chunk_off(64 + r, ch, 128)), x);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] = r < L ? gam * x[c] : 0.f;
+            store_split8(bq, bq + 16384, sw128_chunk_off(r, ch, 64), x);
+        }
+    }
     invert_unit_lower(sA, sY);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -452,10 +470,22 @@ template <int MODE> struct Chain {
     static constexpr uint32_t Q = Scal + 1024;                 // kChainOut
     static constexpr uint32_t Stage = MODE == kChainOut ? Q + 16384 : Scal + 1024;
     static constexpr uint32_t XLo = MODE == kChainOut ? kLo : 8192u;  // from a hi image to its lo one
-    static constexpr uint32_t Img = 2 * Stage;  // kChainStates: S hi, lo (32 KB each), U hi, lo (16 KB each)
-    static constexpr uint32_t Misc = Img + (MODE == kChainStates ? 98304u : 0u);
+    static constexpr uint32_t Misc = 2 * Stage;
     static constexpr uint32_t Smem = Misc + 512 + 2048 + 1024;
 };
+
+// NB 16-byte blocks of row d, from block b0 on, of an unswizzled image and of its lo image behind it
+template <int NB>
+__device__ __forceinline__ void store_blocks(uint8_t* img, uint32_t lo_off, int b0, int d, const uint32_t* hi,
+                                             const uint32_t* lo)
+{
+    uint8_t* p = img + (size_t)b0 * 2048 + d * 16;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        *reinterpret_cast<uint4*>(p + i * 2048) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+        *reinterpret_cast<uint4*>(p + lo_off + i * 2048) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+    }
+}
 
 // token rows L .. 63 of one 64-channel atom column set to zero by a warpgroup
 __device__ __forceinline__ void zero_tail_rows(uint8_t* atom, int L)
@@ -726,19 +756,21 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
         for (int c = 0; c < 32; ++c)
             S[c] = S0 ? pair(S0[srow + (size_t)(2 * c) * 128], S0[srow + (size_t)(2 * c + 1) * 128]) : 0ull;
-        // the state operand of chunk `it`; its last chunk's token rows past the sequence's end hold other
-        // tokens, whose values may be anything, and are cleared before the tensor core reads them
+        // the state operand of chunk `it`, and for the backward its image
         auto put_state = [&](int it) {
+            uint32_t hi[32], lo[32];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int m = 0; m < 16; ++m) split2(S[16 * b + m], hi[m], lo[m]);
-                tmem_st16u(tl + kTmS + 64 * wg + 16 * b, hi);
-                tmem_st16u(tl + kTmS + 64 * wg + 32 + 16 * b, lo);
+                for (int m = 16 * b; m < 16 * b + 16; ++m) split2(S[m], hi[m], lo[m]);
+                tmem_st16u(tl + kTmS + 64 * wg + 16 * b, hi + 16 * b);
+                tmem_st16u(tl + kTmS + 64 * wg + 32 + 16 * b, lo + 16 * b);
             }
             tmem_wait_st();
-            if (it < nch) warp_arrive(bar_s + 8 * wg);
+            if (it < nch) {
+                warp_arrive(bar_s + 8 * wg);
+                if (!kOut) store_blocks<8>(images + ((size_t)(jb + it) * H + h) * kImages + kImgS, 32768, 8 * wg, d, hi, lo);
+            }
         };
         // The last chunk's token rows past the sequence's end hold other tokens, whose values may be anything:
         // cleared before the tensor core reads them.
@@ -795,6 +827,12 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_wait_st();
             warp_arrive(bar_w + 8 * wg);
             if (it + 1 < nch) clear_tail(it + 1);
+            if (!kOut) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int m = 0; m < 16; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
+                store_blocks<4>(images + ((size_t)(jb + it) * H + h) * kImages + kImgU, 16384, 4 * wg, d, hi, lo);
+            }
             ok = ok && mbar_wait_ab(bar_d + 8 * wg, par, s_abort);
             fence_after_sync();
             {
@@ -822,17 +860,30 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-inline size_t slots_bytes(long long units) { return (size_t)units * kSlot; }
-
-inline cudaError_t launch_prep(const CUtensorMap& tq, const CUtensorMap& tk, const float* la, const float* beta,
-                               const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq, int N, int H, int Hk,
-                               long long units, uint8_t* slots, cudaStream_t stream)
+template <bool BWD>
+cudaError_t launch_prep(const CUtensorMap& tq, const CUtensorMap& tk, const float* la, const float* beta,
+                        const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq, int N, int H, int Hk,
+                        long long units, uint8_t* slots, uint8_t* bslots, cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(gdn_prep_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
+    const cudaError_t e = cudaFuncSetAttribute(gdn_prep_kernel<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
     if (e != cudaSuccess) return e;
-    LaunchScope ls("gdn_prep", stream);
-    gdn_prep_kernel<false><<<(unsigned)units, kPrepThreads, kPrepSmem, stream>>>(tq, tk, la, beta, hdr, off, cu, Tseq, N,
-                                                                                H, H / Hk, slots, nullptr);
+    LaunchScope ls(BWD ? "gdn_bwd_prep" : "gdn_prep", stream);
+    gdn_prep_kernel<BWD><<<(unsigned)units, kPrepThreads, kPrepSmem, stream>>>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H,
+                                                                              H / Hk, slots, bslots);
+    return cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t launch_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const float* S0,
+                         float* S_final, void* out, const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq,
+                         int N, int H, int Hk, const uint8_t* slots, uint8_t* images, cudaStream_t stream)
+{
+    using C = Chain<MODE>;
+    const cudaError_t e = cudaFuncSetAttribute(gdn_chain_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
+    if (e != cudaSuccess) return e;
+    LaunchScope ls(MODE == kChainOut ? "gdn_chain" : "gdn_bwd_states", stream);
+    gdn_chain_kernel<MODE><<<(unsigned)(N * H), C::kThreads, C::Smem, stream>>>(
+        tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, hdr, off, cu, Tseq, N, H, H / Hk, slots, images);
     return cudaGetLastError();
 }
 
@@ -849,16 +900,10 @@ inline cudaError_t launch_fwd(const void* q, const void* k, const void* v, const
         if (!make_token_map(&tq, q, true, Hk, Ttot, 64) || !make_token_map(&tk, k, true, Hk, Ttot, 64) ||
             !make_token_map(&tv, v, true, H, Ttot, 64))
             return cudaErrorInvalidValue;
-        e = launch_prep(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, slots, stream);
+        e = launch_prep<false>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, slots, nullptr, stream);
         if (e != cudaSuccess) return e;
     }
-    using C = Chain<kChainOut>;
-    e = cudaFuncSetAttribute(gdn_chain_kernel<kChainOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
-    if (e != cudaSuccess) return e;
-    LaunchScope ls("gdn_chain", stream);
-    gdn_chain_kernel<kChainOut><<<(unsigned)(N * H), C::kThreads, C::Smem, stream>>>(
-        tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, hdr, off, cu, Tseq, N, H, H / Hk, slots, nullptr);
-    return cudaGetLastError();
+    return launch_chain<kChainOut>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, slots, nullptr, stream);
 }
 
 }  // namespace gdn

@@ -16,6 +16,7 @@
 #include "decode.cuh"
 #include "gated_norm.cuh"
 #include "gdn.cuh"
+#include "gdn_bwd_tc.cuh"
 #include "gdn_tc.cuh"
 #include "prefill_simt.cuh"
 #include "prefill_tc.cuh"
