@@ -12,7 +12,7 @@ bool gdn_use_tc(kda_dtype dt, int dk, int dv) { return dt == KDA_BF16 && dk == 1
 struct GdnFwdPlan {
     Plan f;
     bool tc;
-    size_t gate_bytes, slot_bytes, total;
+    size_t gate_bytes, total;
 };
 
 kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, int num_seqs, kda_dtype dt,
@@ -22,8 +22,9 @@ kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, i
     if (st != KDA_OK) return st;
     p.tc = gdn_use_tc(dt, dk, dv);
     p.gate_bytes = p.tc ? 0 : round_up(sizeof(float) * (size_t)p.f.Ttot * H * dk, kAlign);
-    p.slot_bytes = p.tc ? gdn::kSlot : round_up(sizeof(float) * simt_slot_floats(dk, dv), kAlign);
-    p.total = sizeof(WsHeader) + p.f.off_bytes + p.gate_bytes + (size_t)p.f.max_chunks * H * p.slot_bytes;
+    p.total = sizeof(WsHeader) + p.f.off_bytes + p.gate_bytes +
+              (p.tc ? gdn::fwd_bytes(p.f.max_chunks, p.f.N, H)
+                    : (size_t)p.f.max_chunks * H * round_up(sizeof(float) * simt_slot_floats(dk, dv), kAlign));
     return KDA_OK;
 }
 
@@ -42,7 +43,7 @@ kda_status make_gdn_bwd_plan(int B, int T, int H, int Hk, int dk, int dv, bool v
     if (p.tc) {
         p.gate_bytes = 0;
         p.total = sizeof(WsHeader) + p.b.f.off_bytes +
-                  gdn::bwd_layout((long long)p.b.f.max_chunks * H, p.b.f.Ttot, H, Hk != H).total;
+                  gdn::bwd_layout(p.b.f.max_chunks, p.b.f.N, p.b.f.Ttot, H, Hk != H).total;
         return KDA_OK;
     }
     p.gate_bytes = round_up(sizeof(float) * (size_t)p.b.f.Ttot * H * dk, kAlign);

@@ -45,19 +45,29 @@ constexpr int kRThreads = 320;
 constexpr uint32_t kRK = 0, kRDo = 16384, kRGq = 32768, kRP = 65536, kRX = 81920, kRScal = 98304, kRStage = 99328;
 constexpr uint32_t kRMisc = 2 * kRStage, kRSmem = kRMisc + 512 + 1024;
 
+// ENDS: no outputs, only a segment's start cotangent from a zero (the last segment's: the given) end one
+template <bool ENDS>
 __global__ void __launch_bounds__(kRThreads, 1)
 gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_do,
                      const float* __restrict__ dS_final, float* __restrict__ dS0, __nv_bfloat16* __restrict__ dv_out,
                      const WsHeader* __restrict__ hdr, const int* __restrict__ off, const int32_t* __restrict__ cu,
                      int Tseq, int N, int H, int G, const uint8_t* __restrict__ slots,
-                     const uint8_t* __restrict__ bslots, uint8_t* __restrict__ images)
+                     const uint8_t* __restrict__ bslots, uint8_t* __restrict__ images, Segments sg)
 {
     extern __shared__ uint8_t smem_raw[];
     if (hdr->bad) return;
-    const int rank = blockIdx.x / H, h = blockIdx.x - rank * H, n = off[N + 1 + rank];
-    const int jb = off[n], nch = off[n + 1] - jb;
+    const int sidx = blockIdx.x / H, h = blockIdx.x - sidx * H;
+    int n, seg, nseg;
+    if (!find_segment(sidx, off, N, sg, cu != nullptr, n, seg, nseg)) return;
+    if (ENDS && seg == 0) return;  // nothing ends at the first segment's start
+    const int jb = off[n] + seg * sg.len, left = off[n + 1] - jb, nch = seg == nseg - 1 ? left : sg.len;
     long long s0, s1;
     seq_bounds(n, cu, Tseq, s0, s1);
+    s0 += 64LL * seg * sg.len;
+    const float* start = seg == nseg - 1 ? (dS_final ? dS_final + ((size_t)n * H + h) * 16384 : nullptr)
+                                         : ENDS ? nullptr : sg.F + ((size_t)(sidx + 1) * H + h) * 16384;
+    float* end = ENDS ? sg.F + ((size_t)sidx * H + h) * 16384
+                      : dS0 && seg == 0 ? dS0 + ((size_t)n * H + h) * 16384 : nullptr;
     uint8_t* sm = align1024(smem_raw);
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + kRMisc;
@@ -205,11 +215,11 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const int wg = warp >> 2, d = 32 * (warp & 3) + lane;
         const bool odd = lane & 1;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const size_t srow = ((size_t)n * H + h) * 16384 + (size_t)wg * 64 * 128 + d;
+        const size_t srow = (size_t)wg * 64 * 128 + d;
         f32x2 S[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-            S[c] = dS_final ? pair(dS_final[srow + (size_t)(2 * c) * 128], dS_final[srow + (size_t)(2 * c + 1) * 128]) : 0ull;
+            S[c] = start ? pair(start[srow + (size_t)(2 * c) * 128], start[srow + (size_t)(2 * c + 1) * 128]) : 0ull;
         auto put_state = [&](int it) {  // the operand of step `it` and its image, the cotangent after that chunk
             uint32_t hi[32], lo[32];
 #pragma unroll
@@ -222,7 +232,7 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             tmem_wait_st();
             if (it < nch) {
                 warp_arrive(bar_s + 8 * wg);
-                store_blocks<8>(images + ((size_t)(jb + nch - 1 - it) * H + h) * kImages + kImgDs, 32768, 8 * wg, d, hi, lo);
+                if (!ENDS) store_blocks<8>(images + ((size_t)(jb + nch - 1 - it) * H + h) * kImages + kImgDs, 32768, 8 * wg, d, hi, lo);
             }
         };
         auto clear_tail = [&](int it) {
@@ -285,7 +295,7 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             tmem_wait_st();
             warp_arrive(bar_w);
             if (it + 1 < nch) clear_tail(it + 1);
-            {   // while D3 runs: dR's image and dv
+            if (!ENDS) {  // while D3 runs: dR's image and dv
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int m = 0; m < 16; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
@@ -315,13 +325,13 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
             put_state(it + 1);
         }
-        if (dS0 && ok) {
+        if (end && ok) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
                 float a, b;
                 unpair(S[c], a, b);
-                dS0[srow + (size_t)(2 * c) * 128] = a;
-                dS0[srow + (size_t)(2 * c + 1) * 128] = b;
+                end[srow + (size_t)(2 * c) * 128] = a;
+                end[srow + (size_t)(2 * c + 1) * 128] = b;
             }
         }
     }
@@ -676,17 +686,21 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
 }
 
-// bytes behind the header and the chunk table: slots, backward slots, images, and with shared q/k heads fp32 dq, dk
+// bytes behind the header and the chunk table: slots, backward slots, images, segment states (forward,
+// transition, reverse), and with shared q/k heads fp32 dq, dk
 struct BwdLayout {
-    size_t slots, bslots, images, dq, dk, total;
+    size_t slots, bslots, images, segs, seg_bytes, dq, dk, total;
 };
-inline BwdLayout bwd_layout(long long units, long long Ttot, int H, bool grouped)
+inline BwdLayout bwd_layout(int max_chunks, int N, long long Ttot, int H, bool grouped)
 {
     BwdLayout l;
+    const long long units = (long long)max_chunks * H;
     l.slots = 0;
     l.bslots = l.slots + (size_t)units * kSlot;
     l.images = l.bslots + (size_t)units * kBwdSlot;
-    l.dq = l.images + (size_t)units * kImages;
+    l.segs = l.images + (size_t)units * kImages;
+    l.seg_bytes = segments_bytes(max_chunks, N, H);
+    l.dq = l.segs + 3 * l.seg_bytes;
     const size_t acc = grouped ? (size_t)Ttot * H * 128 * sizeof(float) : 0;
     l.dk = l.dq + acc;
     l.total = l.dk + acc;
@@ -701,9 +715,13 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
 {
     alignas(64) CUtensorMap tq{}, tk{}, tv{}, tdo{};
     const long long units = (long long)max_chunks * H;
-    if (units > 0x7fffffffLL || (long long)N * H > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (units > 0x7fffffffLL || ((long long)max_chunks + N) * H > 0x7fffffffLL) return cudaErrorInvalidValue;
     const bool grouped = Hk != H;
-    const BwdLayout lay = bwd_layout(units, Ttot, H, grouped);
+    const BwdLayout lay = bwd_layout(max_chunks, N, Ttot, H, grouped);
+    const int len = Ttot > 0 ? segment_length(max_chunks, N, H) : 0;
+    float* segs = (float*)(ws + lay.segs);
+    const Segments fwd{len, segs, (float*)((uint8_t*)segs + lay.seg_bytes)};
+    const Segments rev{len, (float*)((uint8_t*)segs + 2 * lay.seg_bytes), fwd.M};
     uint8_t *slots = ws + lay.slots, *bslots = ws + lay.bslots, *images = ws + lay.images;
     float *dq_acc = grouped ? (float*)(ws + lay.dq) : nullptr, *dk_acc = grouped ? (float*)(ws + lay.dk) : nullptr;
     cudaError_t e = cudaSuccess;
@@ -713,16 +731,28 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
             return cudaErrorInvalidValue;
         e = launch_prep<true>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, slots, bslots, stream);
         if (e == cudaSuccess)
-            e = launch_chain<kChainStates>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, slots, images,
-                                           stream);
+            e = run_chain<kChainStates>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, max_chunks, slots,
+                                        images, fwd, stream);
         if (e != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(gdn_bwd_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRSmem);
+    e = cudaFuncSetAttribute(gdn_bwd_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(gdn_bwd_chain_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRSmem);
     if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)(max_segments(max_chunks, N, len) * H);
+    if (len) {
+        {
+            LaunchScope ls("gdn_bwd_ends", stream);
+            gdn_bwd_chain_kernel<true><<<grid, kRThreads, kRSmem, stream>>>(
+                tk, tdo, dS_final, nullptr, nullptr, hdr, off, cu, Tseq, N, H, H / Hk, slots, bslots, nullptr, rev);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
+        if ((e = launch_join<true>(hdr, off, N, H, rev, stream)) != cudaSuccess) return e;
+    }
     {
         LaunchScope ls("gdn_bwd_chain", stream);
-        gdn_bwd_chain_kernel<<<(unsigned)(N * H), kRThreads, kRSmem, stream>>>(
-            tk, tdo, dS_final, dS0, (__nv_bfloat16*)dv, hdr, off, cu, Tseq, N, H, H / Hk, slots, bslots, images);
+        gdn_bwd_chain_kernel<false><<<grid, kRThreads, kRSmem, stream>>>(
+            tk, tdo, dS_final, dS0, (__nv_bfloat16*)dv, hdr, off, cu, Tseq, N, H, H / Hk, slots, bslots, images, rev);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (Ttot == 0) return cudaSuccess;

@@ -458,6 +458,60 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 // ----------------------------------------------------------------------------------------------------
 constexpr int kChainOut = 0;     // the prefill: writes out and S_final
 constexpr int kChainStates = 1;  // the backward's recompute: writes each chunk's start state and U
+constexpr int kChainEnds = 2;    // a segment's end state and transition, see below
+
+// Segments.  With few (sequence, head) pairs the chunks' chain would leave most SMs idle, so a sequence is cut
+// into segments of `len` chunks.  Over a segment the state maps affinely, S_end = M S_start + F: one CTA
+// runs the chain from a zero state (F; the first segment's from S0), another from the identity without v
+// (M, whose 128 columns take the place of the value columns); a small kernel then chains the segments
+// (F'_g = M_g F'_{g-1} + F_g is the start state of segment g + 1) and the real pass runs all segments at once.
+// The reverse chain's transition is M's transpose.  Segments of all sequences are numbered in order; every
+// sequence has at least one.
+struct Segments {
+    int len;          // chunks a segment; 0: one segment a sequence, longest sequences first
+    float* F;         // [segment][H][128][128]: end states, then start states of the segment after
+    float* M;         // [segment][H][128][128]
+};
+
+// segment idx -> its sequence, number and the sequence's count; false past the last one (whole warps)
+__device__ __forceinline__ bool find_segment(int idx, const int* __restrict__ off, int N, const Segments& sg, bool varlen,
+                                             int& n, int& seg, int& nseg)
+{
+    if (sg.len == 0) {
+        n = off[N + 1 + idx];
+        seg = 0;
+        nseg = 1;
+        return true;
+    }
+    if (!varlen) {
+        nseg = max(1, (off[1] - off[0] + sg.len - 1) / sg.len);
+        n = idx / nseg;
+        seg = idx - n * nseg;
+        return n < N;
+    }
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int n0 = 0; n0 < N; n0 += 32) {
+        const int m = n0 + lane;
+        const int cnt = m < N ? max(1, (off[m + 1] - off[m] + sg.len - 1) / sg.len) : 0;
+        int inc = cnt;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, idx < base + inc);
+        if (hit) {
+            const int f = __ffs(hit) - 1;
+            n = n0 + f;
+            nseg = __shfl_sync(0xffffffffu, cnt, f);
+            seg = idx - base - __shfl_sync(0xffffffffu, inc - cnt, f);
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return false;
+}
 
 constexpr uint32_t kTmD1 = 0, kTmDq = 64, kTmU = 128, kTmPo = 192, kTmS = 256, kTmUw = 384;
 
@@ -500,16 +554,26 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_v, const float* S0, float* S_final,
                  __nv_bfloat16* __restrict__ out, const WsHeader* __restrict__ hdr, const int* __restrict__ off,
                  const int32_t* __restrict__ cu, int Tseq, int N, int H, int G, const uint8_t* __restrict__ slots,
-                 uint8_t* __restrict__ images)
+                 uint8_t* __restrict__ images, Segments sg)
 {
     using C = Chain<MODE>;
     constexpr bool kOut = MODE == kChainOut;
     extern __shared__ uint8_t smem_raw[];
     if (hdr->bad) return;
-    const int rank = blockIdx.x / H, h = blockIdx.x - rank * H, n = off[N + 1 + rank];
-    const int jb = off[n], nch = off[n + 1] - jb;
+    const int sidx = blockIdx.x / H, h = blockIdx.x - sidx * H;
+    const bool trans = MODE == kChainEnds && blockIdx.y == 1;  // from the identity, without v
+    int n, seg, nseg;
+    if (!find_segment(sidx, off, N, sg, cu != nullptr, n, seg, nseg)) return;
+    // nothing starts from the last segment's end, and the first one's start is known
+    if (MODE == kChainEnds && (seg == nseg - 1 || (trans && seg == 0))) return;
+    const int jb = off[n] + seg * sg.len, left = off[n + 1] - jb, nch = seg == nseg - 1 ? left : sg.len;
     long long s0, s1;
     seq_bounds(n, cu, Tseq, s0, s1);
+    s0 += 64LL * seg * sg.len;
+    const float* start = seg == 0 ? (S0 ? S0 + ((size_t)n * H + h) * 16384 : nullptr)
+                                  : MODE == kChainEnds ? nullptr : sg.F + ((size_t)(sidx - 1) * H + h) * 16384;
+    float* end = MODE == kChainEnds ? (trans ? sg.M : sg.F) + ((size_t)sidx * H + h) * 16384
+                                    : S_final && seg == nseg - 1 ? S_final + ((size_t)n * H + h) * 16384 : nullptr;
     uint8_t* sm = align1024(smem_raw);
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + C::Misc;
@@ -593,7 +657,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ok = ok && warp_wait(bar_full + 8 * (it & 1), (uint32_t)(it >> 1) & 1u, s_abort);
             ok = ok && warp_wait(bar_z, (uint32_t)it & 1u, s_abort);
             fence_after_sync();
-            if (ok && elect_one()) v_times(tmem + kTmU, desc_mnmajor(st + C::V, 64, 0), desc_kmajor(st + C::Slot, 64, 0), 1);
+            if (!trans && ok && elect_one()) v_times(tmem + kTmU, desc_mnmajor(st + C::V, 64, 0), desc_kmajor(st + C::Slot, 64, 0), 1);
             __syncwarp();
         };
         if (nch > 0) issue_v(0);
@@ -649,9 +713,9 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ok = ok && warp_wait(bar_r, par, s_abort);
             fence_after_sync();
             if (ok && elect_one()) {
-                r_times(tmem + kTmU, dX, 0, id32, 0);
+                r_times(tmem + kTmU, dX, 0, id32, trans);
                 mma_commit(bar_u);
-                r_times(tmem + kTmU + 32, dX + (uint64_t)(4096 >> 4), 0, id32, 0);
+                r_times(tmem + kTmU + 32, dX + (uint64_t)(4096 >> 4), 0, id32, trans);
             }
             __syncwarp();
             ok = ok && warp_wait(bar_r + 8, par, s_abort);
@@ -750,12 +814,15 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else {
         const int wg = warp >> 2, d = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const size_t srow = ((size_t)n * H + h) * 16384 + (size_t)wg * 64 * 128 + d;
+        const size_t srow = (size_t)wg * 64 * 128 + d;
         if (kOut) regs_inc<176>();
         f32x2 S[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-            S[c] = S0 ? pair(S0[srow + (size_t)(2 * c) * 128], S0[srow + (size_t)(2 * c + 1) * 128]) : 0ull;
+        for (int c = 0; c < 32; ++c) {
+            const int ch = 64 * wg + 2 * c;
+            S[c] = start ? pair(start[srow + (size_t)(2 * c) * 128], start[srow + (size_t)(2 * c + 1) * 128])
+                         : trans ? pair(ch == d ? 1.f : 0.f, ch + 1 == d ? 1.f : 0.f) : 0ull;
+        }
         // the state operand of chunk `it`, and for the backward its image
         auto put_state = [&](int it) {
             uint32_t hi[32], lo[32];
@@ -769,7 +836,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_wait_st();
             if (it < nch) {
                 warp_arrive(bar_s + 8 * wg);
-                if (!kOut) store_blocks<8>(images + ((size_t)(jb + it) * H + h) * kImages + kImgS, 32768, 8 * wg, d, hi, lo);
+                if (MODE == kChainStates) store_blocks<8>(images + ((size_t)(jb + it) * H + h) * kImages + kImgS, 32768, 8 * wg, d, hi, lo);
             }
         };
         // The last chunk's token rows past the sequence's end hold other tokens, whose values may be anything:
@@ -827,7 +894,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_wait_st();
             warp_arrive(bar_w + 8 * wg);
             if (it + 1 < nch) clear_tail(it + 1);
-            if (!kOut) {
+            if (MODE == kChainStates) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int m = 0; m < 16; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
@@ -845,13 +912,13 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             put_state(it + 1);
         }
-        if (S_final && ok) {
+        if (end && ok) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
                 float a, b;
                 unpair(S[c], a, b);
-                S_final[srow + (size_t)(2 * c) * 128] = a;
-                S_final[srow + (size_t)(2 * c + 1) * 128] = b;
+                end[srow + (size_t)(2 * c) * 128] = a;
+                end[srow + (size_t)(2 * c + 1) * 128] = b;
             }
         }
     }
@@ -873,37 +940,161 @@ cudaError_t launch_prep(const CUtensorMap& tq, const CUtensorMap& tk, const floa
     return cudaGetLastError();
 }
 
+// F'_g = M_g F'_{g-1} + F_g over the inner segments of a sequence (forward), or, with the transposes and
+// from the last segment down, F'_g = M_g^T F'_{g+1} + F_g (reverse).  One CTA a (sequence, head, 16 value
+// columns); thread = key channel.  fp32 on CUDA cores: about 4 us a segment, all heads at once.
+constexpr int kJoinCols = 16;
+template <bool REVERSE>
+__global__ void __launch_bounds__(128)
+gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, int N, int H, Segments sg)
+{
+    __shared__ __align__(16) float sS[128][kJoinCols];
+    if (hdr->bad) return;
+    const int n = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * kJoinCols, ch = threadIdx.x;
+    // the sequence's first segment: the segments of those before it
+    int part = 0;
+    for (int m = ch; m < n; m += 128) part += max(1, (off[m + 1] - off[m] + sg.len - 1) / sg.len);
+    __shared__ int s_first;
+    if (ch == 0) s_first = 0;
+    __syncthreads();
+    if (part) atomicAdd(&s_first, part);
+    __syncthreads();
+    const int first = s_first, nseg = (off[n + 1] - off[n] + sg.len - 1) / sg.len;
+    for (int i = 0; i + 2 < nseg; ++i) {
+        const int g = REVERSE ? nseg - 2 - i : 1 + i, from = REVERSE ? g + 1 : g - 1;
+        const size_t at = ((size_t)(first + g) * H + h) * 16384;
+        const float* src = sg.F + ((size_t)(first + from) * H + h) * 16384;
+        float acc[kJoinCols];
+        float4* dst = reinterpret_cast<float4*>(sg.F + at + (size_t)ch * 128 + v0);
+#pragma unroll
+        for (int m = 0; m < kJoinCols; m += 4) {
+            // the state before this step: its own F' as this thread left it, or the first one read
+            if (i == 0) *reinterpret_cast<float4*>(&sS[ch][m]) = *reinterpret_cast<const float4*>(src + (size_t)ch * 128 + v0 + m);
+            const float4 f = dst[m / 4];
+            acc[m] = f.x; acc[m + 1] = f.y; acc[m + 2] = f.z; acc[m + 3] = f.w;
+        }
+        __syncthreads();
+        const float* M = sg.M + at;
+#pragma unroll 2
+        for (int c = 0; c < 128; c += 4) {
+            float w[4];
+            if (REVERSE) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = M[(size_t)(c + k) * 128 + ch];
+            } else {
+                const float4 w4 = *reinterpret_cast<const float4*>(M + (size_t)ch * 128 + c);
+                w[0] = w4.x; w[1] = w4.y; w[2] = w4.z; w[3] = w4.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int m = 0; m < kJoinCols; ++m) acc[m] = fmaf(w[k], sS[c + k][m], acc[m]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < kJoinCols; m += 4) {
+            const float4 f = make_float4(acc[m], acc[m + 1], acc[m + 2], acc[m + 3]);
+            dst[m / 4] = f;
+            *reinterpret_cast<float4*>(&sS[ch][m]) = f;
+        }
+    }
+}
+
+// Chunks a segment, from the number of chains and their length (for packed sequences the mean; the lengths
+// are on the device).  Modelled in microseconds: a chunk costs 2.9 in the real pass and 2.3 in the ends', the
+// join 4 a segment, and the CTAs of a pass run in waves of one an SM.  Measured at 512 chunks x 32 heads.
+inline int segment_length(int max_chunks, int N, int H)
+{
+    constexpr int kSms = 148, kMaxSeqs = 1024, kMinLen = 4;
+    if (N > kMaxSeqs || max_chunks == 0) return 0;
+    const long long chains = (long long)N * H;
+    const int L = (max_chunks + N - 1) / N;
+    auto waves = [&](long long ctas) { return (double)((ctas + kSms - 1) / kSms); };
+    double best = waves(chains) * L * 2.9;
+    int len = 0;
+    for (int g = 2; g <= 64 && L / g >= kMinLen; ++g) {
+        const int l = (L + g - 1) / g;
+        const double t = waves(chains * g) * l * 2.9 + waves(chains * (2 * g - 3)) * l * 2.3 + 4.0 * (g - 2) + 10.0;
+        if (t < 0.95 * best) {
+            best = t;
+            len = l;
+        }
+    }
+    return len;
+}
+inline long long max_segments(int max_chunks, int N, int len) { return len ? max_chunks / len + N : N; }
+inline size_t segments_bytes(int max_chunks, int N, int H)
+{
+    const int len = segment_length(max_chunks, N, H);
+    return len ? (size_t)max_segments(max_chunks, N, len) * H * 65536 : 0;
+}
+
 template <int MODE>
 cudaError_t launch_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const float* S0,
                          float* S_final, void* out, const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq,
-                         int N, int H, int Hk, const uint8_t* slots, uint8_t* images, cudaStream_t stream)
+                         int N, int H, int Hk, int max_chunks, const uint8_t* slots, uint8_t* images, const Segments& sg,
+                         cudaStream_t stream)
 {
     using C = Chain<MODE>;
     const cudaError_t e = cudaFuncSetAttribute(gdn_chain_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
     if (e != cudaSuccess) return e;
-    LaunchScope ls(MODE == kChainOut ? "gdn_chain" : "gdn_bwd_states", stream);
-    gdn_chain_kernel<MODE><<<(unsigned)(N * H), C::kThreads, C::Smem, stream>>>(
-        tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, hdr, off, cu, Tseq, N, H, H / Hk, slots, images);
+    LaunchScope ls(MODE == kChainOut ? "gdn_chain" : MODE == kChainStates ? "gdn_bwd_states" : "gdn_ends", stream);
+    const dim3 grid((unsigned)(max_segments(max_chunks, N, sg.len) * H), MODE == kChainEnds ? 2 : 1);
+    gdn_chain_kernel<MODE><<<grid, C::kThreads, C::Smem, stream>>>(tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, hdr, off,
+                                                                  cu, Tseq, N, H, H / Hk, slots, images, sg);
     return cudaGetLastError();
+}
+template <bool REVERSE>
+cudaError_t launch_join(const WsHeader* hdr, const int* off, int N, int H, const Segments& sg, cudaStream_t stream)
+{
+    LaunchScope ls("gdn_join", stream);
+    gdn_join_kernel<REVERSE><<<dim3(N, H, 128 / kJoinCols), 128, 0, stream>>>(hdr, off, N, H, sg);
+    return cudaGetLastError();
+}
+
+// the chain of all sequences, segmented where that pays; seg_ws: twice segments_bytes()
+template <int MODE>
+cudaError_t run_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const float* S0,
+                      float* S_final, void* out, const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq, int N,
+                      int H, int Hk, int max_chunks, const uint8_t* slots, uint8_t* images, Segments sg,
+                      cudaStream_t stream)
+{
+    if (sg.len) {
+        cudaError_t e = launch_chain<kChainEnds>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, max_chunks,
+                                                 slots, nullptr, sg, stream);
+        if (e == cudaSuccess) e = launch_join<false>(hdr, off, N, H, sg, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_chain<MODE>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, max_chunks, slots, images, sg,
+                              stream);
+}
+
+// bytes behind the header and the chunk table
+inline size_t fwd_bytes(int max_chunks, int N, int H)
+{
+    return (size_t)max_chunks * H * kSlot + 2 * segments_bytes(max_chunks, N, H);
 }
 
 inline cudaError_t launch_fwd(const void* q, const void* k, const void* v, const float* la, const float* beta,
                               const float* S0, float* S_final, void* out, const WsHeader* hdr, const int* off,
                               const int32_t* cu, int Tseq, int N, int H, int Hk, int max_chunks, long long Ttot,
-                              uint8_t* slots, cudaStream_t stream)
+                              uint8_t* ws, cudaStream_t stream)
 {
     alignas(64) CUtensorMap tq{}, tk{}, tv{};
     const long long units = (long long)max_chunks * H;
-    if (units > 0x7fffffffLL || (long long)N * H > 0x7fffffffLL) return cudaErrorInvalidValue;
-    cudaError_t e = cudaSuccess;
+    if (units > 0x7fffffffLL || ((long long)max_chunks + N) * H > 0x7fffffffLL) return cudaErrorInvalidValue;
+    uint8_t* segs = ws + units * kSlot;
+    const size_t sb = segments_bytes(max_chunks, N, H);
+    const Segments sg{Ttot > 0 ? segment_length(max_chunks, N, H) : 0, (float*)segs, (float*)(segs + sb)};
     if (Ttot > 0) {
         if (!make_token_map(&tq, q, true, Hk, Ttot, 64) || !make_token_map(&tk, k, true, Hk, Ttot, 64) ||
             !make_token_map(&tv, v, true, H, Ttot, 64))
             return cudaErrorInvalidValue;
-        e = launch_prep<false>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, slots, nullptr, stream);
+        const cudaError_t e = launch_prep<false>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, ws, nullptr, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_chain<kChainOut>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, slots, nullptr, stream);
+    return run_chain<kChainOut>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, max_chunks, ws, nullptr, sg,
+                                stream);
 }
 
 }  // namespace gdn
