@@ -127,9 +127,8 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar)
 }
 
 // ---- workspace slot of one (chunk, head) ---------------------------------------------------------------
-// 64 x 64 SW128 images, X above Y so that one MMA can run over both: X hi, Y hi, X lo, Y lo; then fp32 rows
-// of 64: 2^g, 2^(g_C - g), beta, -2^g.
-constexpr uint32_t kYofX = 8192, kLo = 16384, kScal = 32768;
+// 64 x 64 SW128 images X hi, X lo, Y hi, Y lo; then fp32 rows of 64: 2^g, 2^(g_C - g), beta, -2^g.
+constexpr uint32_t kLo = 8192, kYofX = 16384, kScal = 32768;
 constexpr uint32_t kSlot = kScal + 1024;
 constexpr int kGam = 0, kW = 64, kBeta = 128, kNgam = 192;  // float offsets in the scalar rows
 // The backward also takes P, (I + A)^-1 and 2^g q (64 x 128): hi and lo of each.
@@ -144,94 +143,86 @@ constexpr uint32_t kImgS = 0, kImgDs = 65536, kImgU = 131072, kImgDr = 163840, k
 // Per-chunk kernel: X, P and the scalar rows of each (chunk, head).
 //
 // One CTA of 256 threads a unit.  [k; q] k^T is one M = 128, N = 64 batch; its epilogue masks and decays
-// the 128 x 64 result.  The inverse comes from recursive doubling over 16 x 16 blocks in fp32 on CUDA
+// the 128 x 64 result.  The inverse comes from recursive doubling over 8 x 8 blocks in fp32 on CUDA
 // cores: the product form's powers of A would lose the small entries, and the split images need X to 16
 // bits.  Y is a split M = 64 product.  Bound by the latency of that dependent chain, so CTAs are kept
-// small (75 KB) to run three an SM.
+// small (57 KB, 64 registers) to run four an SM: A lies where Y will, over the consumed [k; q] tile.
 // ----------------------------------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
 constexpr uint32_t kPrepP = kSlot;                      // P hi, lo; the slot takes the [k; q] tile's place
-constexpr uint32_t kPrepA = kPrepP + 16384;             // A / X fp32 [64][68]
-constexpr uint32_t kPrepY = kPrepA + 64 * kAS * 4;      // scratch [32][36]
+constexpr uint32_t kPrepA = kYofX;                      // A / inverse fp32 [64][68], to the slot's end
+constexpr uint32_t kPrepY = kPrepP + 16384;             // scratch [32][36]
 constexpr uint32_t kPrepMisc = kPrepY + 32 * 36 * 4;    // g, beta, barriers
 constexpr uint32_t kPrepSmem = kPrepMisc + 1024 + 1024;
+static_assert(kPrepA + 64 * kAS * 4 <= kSlot, "A fits behind X");
+
+// rows b + K .., columns b .. of the inverse from the K x K blocks beside them, -X_11 (A_10 X_00): `t` numbers
+// the 2 x 2 tiles of the block.  Small tiles: a chain of few loads, spread over the CTA.
+template <int K>
+__device__ __forceinline__ void merge_blocks(float* __restrict__ sA, float* __restrict__ sY, int t)
+{
+    constexpr int kTiles = (K / 2) * (K / 2);
+    const bool active = t < 64 / (2 * K) * kTiles;
+    const int b = 2 * K * (t / kTiles), r = 2 * (t % kTiles / (K / 2)), c = 2 * (t % (K / 2));
+    float* y = sY + (b >> 1) * 36;  // K rows a pair
+    auto product = [&](const float* P, int ps, const float* Q, int qs, float (&d)[2][2]) {
+        d[0][0] = d[0][1] = d[1][0] = d[1][1] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; k += 4) {
+            const float4 p0 = *reinterpret_cast<const float4*>(P + k), p1 = *reinterpret_cast<const float4*>(P + ps + k);
+            const float a0[4] = {p0.x, p0.y, p0.z, p0.w}, a1[4] = {p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 q = *reinterpret_cast<const float2*>(Q + (k + e) * qs);
+                d[0][0] = fmaf(a0[e], q.x, d[0][0]); d[0][1] = fmaf(a0[e], q.y, d[0][1]);
+                d[1][0] = fmaf(a1[e], q.x, d[1][0]); d[1][1] = fmaf(a1[e], q.y, d[1][1]);
+            }
+        }
+    };
+    float d[2][2];
+    if (active) {
+        product(sA + (b + K + r) * kAS + b, kAS, sA + b * kAS + b + c, kAS, d);
+        *reinterpret_cast<float2*>(y + r * 36 + c) = make_float2(d[0][0], d[0][1]);
+        *reinterpret_cast<float2*>(y + (r + 1) * 36 + c) = make_float2(d[1][0], d[1][1]);
+    }
+    __syncthreads();
+    if (active) {
+        product(sA + (b + K + r) * kAS + b + K, kAS, y + c, 36, d);
+        *reinterpret_cast<float2*>(sA + (b + K + r) * kAS + b + c) = make_float2(-d[0][0], -d[0][1]);
+        *reinterpret_cast<float2*>(sA + (b + K + r + 1) * kAS + b + c) = make_float2(-d[1][0], -d[1][1]);
+    }
+    __syncthreads();
+}
 
 // (I + A)^-1 in place over a strictly lower 64 x 64 A (row stride kAS, zero on and above the diagonal)
 __device__ __forceinline__ void invert_unit_lower(float* __restrict__ sA, float* __restrict__ sY)
 {
     const int tid = threadIdx.x;
-    {   // the four diagonal blocks: thread -> (block, column), forward substitution
-        const int b = 16 * (tid >> 4), jj = tid & 15;
-        float x[16];
+    {   // the eight 8 x 8 diagonal blocks: thread -> (block, column), forward substitution
+        const int b = 8 * (tid >> 3), jj = tid & 7;
+        float x[8];
         if (tid < 64) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < 8; ++r) {
+                const float4 p = *reinterpret_cast<const float4*>(sA + (b + r) * kAS + b);
+                const float4 q = *reinterpret_cast<const float4*>(sA + (b + r) * kAS + b + 4);
+                const float av[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
                 float s = 0.f;
 #pragma unroll
-                for (int i4 = 0; i4 < r; i4 += 4) {
-                    const float4 a4 = *reinterpret_cast<const float4*>(sA + (b + r) * kAS + b + i4);
-                    const float av[4] = {a4.x, a4.y, a4.z, a4.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (i4 + j < r) s = fmaf(av[j], x[i4 + j], s);
-                }
+                for (int i = 0; i < r; ++i) s = fmaf(av[i], x[i], s);
                 x[r] = (r == jj) ? 1.f : ((r < jj) ? 0.f : -s);
             }
         }
         __syncthreads();
         if (tid < 64) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) sA[(b + r) * kAS + b + jj] = x[r];
+            for (int r = 0; r < 8; ++r) sA[(b + r) * kAS + b + jj] = x[r];
         }
         __syncthreads();
     }
-    {   // X_10 = -X_11 A_10 X_00 in each 32 x 32 half: thread -> (half, row, 4 columns)
-        const int p = tid >> 6, ra = (tid >> 2) & 15, cc = (tid & 3) * 4;
-        const int bi = 32 * p + 16, bj = 32 * p;
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-        if (tid < 128) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float a = sA[(bi + ra) * kAS + bj + k];
-                const float4 x4 = *reinterpret_cast<const float4*>(sA + (bj + k) * kAS + bj + cc);
-                y[0] = fmaf(a, x4.x, y[0]); y[1] = fmaf(a, x4.y, y[1]); y[2] = fmaf(a, x4.z, y[2]); y[3] = fmaf(a, x4.w, y[3]);
-            }
-            *reinterpret_cast<float4*>(sY + (p * 16 + ra) * 36 + cc) = make_float4(y[0], y[1], y[2], y[3]);
-        }
-        __syncthreads();
-        if (tid < 128) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float a = sA[(bi + ra) * kAS + bi + k];
-                const float4 y4 = *reinterpret_cast<const float4*>(sY + (p * 16 + k) * 36 + cc);
-                x[0] = fmaf(a, y4.x, x[0]); x[1] = fmaf(a, y4.y, x[1]); x[2] = fmaf(a, y4.z, x[2]); x[3] = fmaf(a, y4.w, x[3]);
-            }
-            *reinterpret_cast<float4*>(sA + (bi + ra) * kAS + bj + cc) = make_float4(-x[0], -x[1], -x[2], -x[3]);
-        }
-        __syncthreads();
-    }
-    {   // the 32 x 32 block below the diagonal: thread -> (row, 4 columns)
-        const int ra = tid >> 3, cc = (tid & 7) * 4;
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float a = sA[(32 + ra) * kAS + k];
-            const float4 x4 = *reinterpret_cast<const float4*>(sA + k * kAS + cc);
-            y[0] = fmaf(a, x4.x, y[0]); y[1] = fmaf(a, x4.y, y[1]); y[2] = fmaf(a, x4.z, y[2]); y[3] = fmaf(a, x4.w, y[3]);
-        }
-        *reinterpret_cast<float4*>(sY + ra * 36 + cc) = make_float4(y[0], y[1], y[2], y[3]);
-        __syncthreads();
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float a = sA[(32 + ra) * kAS + 32 + k];
-            const float4 y4 = *reinterpret_cast<const float4*>(sY + k * 36 + cc);
-            x[0] = fmaf(a, y4.x, x[0]); x[1] = fmaf(a, y4.y, x[1]); x[2] = fmaf(a, y4.z, x[2]); x[3] = fmaf(a, y4.w, x[3]);
-        }
-        *reinterpret_cast<float4*>(sA + (32 + ra) * kAS + cc) = make_float4(-x[0], -x[1], -x[2], -x[3]);
-        __syncthreads();
-    }
+    merge_blocks<8>(sA, sY, tid);
+    merge_blocks<16>(sA, sY, tid);
+    merge_blocks<32>(sA, sY, tid);
 }
 
 // g (log2 units, cumulative) and beta of a chunk's 64 tokens into shared memory, by one warp; tokens past
@@ -273,7 +264,7 @@ __device__ __forceinline__ void store_split8(uint8_t* hi, uint8_t* lo, uint32_t 
 }
 
 template <bool BWD>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 4)
 gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const float* __restrict__ la, const float* __restrict__ beta, const WsHeader* __restrict__ hdr,
                 const int* __restrict__ off, const int32_t* __restrict__ cu, int Tseq, int N, int H, int G,
@@ -332,6 +323,20 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     ok = __syncthreads_and(ok);
     ok = ok && mbar_wait(bar_mma, 0);
     fence_after_sync();
+    if (BWD) {  // 2^g q, before A takes the tile's place
+        uint8_t* bq = bslots + (size_t)blockIdx.x * kBwdSlot + kBwdQ;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int e = tid + kPrepThreads * m, r = e >> 4, ch = e & 15;
+            const float gam = ex2_approx(s_g[r]);
+            float x[8];
+            unpack8(*reinterpret_cast<const uint4*>(sm + sw128_chunk_off(64 + r, ch, 128)), x);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] = r < L ? gam * x[c] : 0.f;
+            store_split8(bq, bq + 16384, sw128_chunk_off(r, ch, 64), x);
+        }
+        __syncthreads();
+    }
     // lanes 0..63: k_i.k_j, lanes 64..127: q_i.k_j; warps 0-3 columns 0..31, warps 4-7 columns 32..63
     const int wq = warp & 3, col0 = (warp >> 2) * 32, i = 32 * (wq & 1) + lane;
     uint8_t* img = sm;  // the [k; q] tile is consumed: the images take its place
@@ -339,13 +344,22 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         float x[32];
         tmem_ld32(tmem + ((uint32_t)(32 * wq) << 16) + col0, x);
         const float gi = s_g[i], bi = s_b[i];
-        const bool row = i < L, isA = wq < 2;
+        const bool row = i < L, isA = wq < 2, above = col0 > 32 * (wq & 1);  // above the diagonal: zero
 #pragma unroll
-        for (int m = 0; m < 32; ++m) {
-            const int j = col0 + m;
-            // the select comes last: what lies past the chunk's end may be anything
-            const float y = x[m] * ex2_approx(gi - s_g[j]);
-            x[m] = (row && (isA ? j < i : j <= i)) ? y : 0.f;
+        for (int m = 0; m < 32; m += 4) {
+            if (above) {
+                x[m] = x[m + 1] = x[m + 2] = x[m + 3] = 0.f;
+                continue;
+            }
+            const float4 g4 = *reinterpret_cast<const float4*>(s_g + col0 + m);
+            const float gj[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = col0 + m + e;
+                // the select comes last: what lies past the chunk's end may be anything
+                const float y = x[m + e] * ex2_approx(gi - gj[e]);
+                x[m + e] = (row && (isA ? j < i : j <= i)) ? y : 0.f;
+            }
         }
         if (isA) {
 #pragma unroll
@@ -360,19 +374,6 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
     fence_before_sync();
     __syncthreads();
-    if (BWD) {  // 2^g q, before the images take the tile's place
-        uint8_t* bq = bslots + (size_t)blockIdx.x * kBwdSlot + kBwdQ;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int e = tid + kPrepThreads * m, r = e >> 4, ch = e & 15;
-            const float gam = ex2_approx(s_g[r]);
-            float x[8];
-            unpack8(*reinterpret_cast<const uint4*>(sm + sw128_chunk_off(64 + r, ch, 128)), x);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = r < L ? gam * x[c] : 0.f;
-            store_split8(bq, bq + 16384, sw128_chunk_off(r, ch, 64), x);
-        }
-    }
     invert_unit_lower(sA, sY);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -388,7 +389,10 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         for (int c = 0; c < 8; ++c) x[c] *= s_b[8 * ch + c];
         store_split8(img, img + kLo, sw128_chunk_off(r, ch, 64), x);
     }
-    if (tid < 64) {
+    fence_proxy_async();
+    fence_before_sync();
+    __syncthreads();
+    if (tid < 64) {  // over A's end
         float* sc = reinterpret_cast<float*>(img + kScal);
         const float gam = ex2_approx(s_g[tid]);
         sc[kGam + tid] = gam;
@@ -396,9 +400,6 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         sc[kBeta + tid] = s_b[tid];
         sc[kNgam + tid] = -gam;
     }
-    fence_proxy_async();
-    fence_before_sync();
-    __syncthreads();
     if (warp == 0) {
         fence_after_sync();
         if (elect_one()) {  // Y = P X
@@ -519,11 +520,10 @@ template <int MODE> struct Chain {
     // 8 compute warps, [4 output warps], MMA, copies [, 2 idle: registers are shared out by warpgroup]
     static constexpr int kThreads = MODE == kChainOut ? 512 : 320;
     static constexpr int kMmaWarp = MODE == kChainOut ? 12 : 8;
-    static constexpr uint32_t K = 0, V = 16384, Slot = 32768;  // (kChainStates: X hi, X lo, scalars)
+    static constexpr uint32_t K = 0, V = 16384, Slot = 32768;  // (without outputs: X hi, X lo, scalars)
     static constexpr uint32_t Scal = Slot + (MODE == kChainOut ? kScal : 16384u);
     static constexpr uint32_t Q = Scal + 1024;                 // kChainOut
     static constexpr uint32_t Stage = MODE == kChainOut ? Q + 16384 : Scal + 1024;
-    static constexpr uint32_t XLo = MODE == kChainOut ? kLo : 8192u;  // from a hi image to its lo one
     static constexpr uint32_t Misc = 2 * Stage;
     static constexpr uint32_t Smem = Misc + 512 + 2048 + 1024;
 };
@@ -630,8 +630,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (kOut) {
                     bulk_g2s(st + C::Slot, slot, kSlot, f);
                 } else {
-                    bulk_g2s(st + C::Slot, slot, 8192, f);
-                    bulk_g2s(st + C::Slot + 8192, slot + kLo, 8192, f);
+                    bulk_g2s(st + C::Slot, slot, 16384, f);
                     bulk_g2s(st + C::Scal, slot + kScal, 1024, f);
                 }
             }
@@ -648,7 +647,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int kk = 0; kk < 4; ++kk) {
                 const uint64_t a = dv + (uint64_t)((kk * 2048) >> 4), bb = b + (uint64_t)((kk * 32) >> 4);
                 mma_bf16(d, a, bb, idv, kk > 0 || !first);
-                mma_bf16(d, a, bb + (C::XLo >> 4), idv, 1);
+                mma_bf16(d, a, bb + (kLo >> 4), idv, 1);
             }
         };
         // U = v^T X^T of chunk `it`, into the accumulator that the chunk before has been read from
@@ -685,7 +684,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     const uint64_t bb = b + (uint64_t)((a * 64 + kk * 32) >> 4);
                     mma_ts(d, x, bb, id, kk > 0 || !first);
                     mma_ts(d, x + 16, bb, id, 1);
-                    mma_ts(d, x, bb + (C::XLo >> 4), id, 1);
+                    mma_ts(d, x, bb + (kLo >> 4), id, 1);
                 }
             };
             ok = ok && warp_wait(bar_s, par, s_abort);
@@ -942,79 +941,94 @@ cudaError_t launch_prep(const CUtensorMap& tq, const CUtensorMap& tk, const floa
 
 // F'_g = M_g F'_{g-1} + F_g over the inner segments of a sequence (forward), or, with the transposes and
 // from the last segment down, F'_g = M_g^T F'_{g+1} + F_g (reverse).  One CTA a (sequence, head, 16 value
-// columns); thread = key channel.  fp32 on CUDA cores: about 4 us a segment, all heads at once.
-constexpr int kJoinCols = 16;
+// columns), M in shared memory; a lane holds half a column of the state in registers (column lane % 16, key
+// channels 64 (lane / 16) ..) and a warp makes 16 rows, so that M is read as broadcasts.  fp32 on CUDA cores.
+constexpr int kJoinCols = 16, kJoinThreads = 256;
+constexpr uint32_t kJoinSmem = 65536 + 1024;
 template <bool REVERSE>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinThreads)
 gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, int N, int H, Segments sg)
 {
-    __shared__ __align__(16) float sS[128][kJoinCols];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_first;
+    __shared__ __align__(8) uint64_t s_bar;
     if (hdr->bad) return;
-    const int n = blockIdx.x, h = blockIdx.y, v0 = blockIdx.z * kJoinCols, ch = threadIdx.x;
+    const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int v = blockIdx.z * kJoinCols + (lane & 15), k0 = 64 * (lane >> 4);
+    uint8_t* sm = align1024(smem_raw);
+    const float* sM = reinterpret_cast<const float*>(sm);
+    const uint32_t bar = smem_u32(&s_bar);
     // the sequence's first segment: the segments of those before it
     int part = 0;
-    for (int m = ch; m < n; m += 128) part += max(1, (off[m + 1] - off[m] + sg.len - 1) / sg.len);
-    __shared__ int s_first;
-    if (ch == 0) s_first = 0;
+    for (int m = threadIdx.x; m < n; m += kJoinThreads) part += max(1, (off[m + 1] - off[m] + sg.len - 1) / sg.len);
+    if (threadIdx.x == 0) {
+        s_first = 0;
+        mbar_init(bar, 1);
+        mbar_fence_init();
+    }
     __syncthreads();
     if (part) atomicAdd(&s_first, part);
     __syncthreads();
     const int first = s_first, nseg = (off[n + 1] - off[n] + sg.len - 1) / sg.len;
+    auto at = [&](int g) { return ((size_t)(first + g) * H + h) * 16384; };
     for (int i = 0; i + 2 < nseg; ++i) {
         const int g = REVERSE ? nseg - 2 - i : 1 + i, from = REVERSE ? g + 1 : g - 1;
-        const size_t at = ((size_t)(first + g) * H + h) * 16384;
-        const float* src = sg.F + ((size_t)(first + from) * H + h) * 16384;
-        float acc[kJoinCols];
-        float4* dst = reinterpret_cast<float4*>(sg.F + at + (size_t)ch * 128 + v0);
-#pragma unroll
-        for (int m = 0; m < kJoinCols; m += 4) {
-            // the state before this step: its own F' as this thread left it, or the first one read
-            if (i == 0) *reinterpret_cast<float4*>(&sS[ch][m]) = *reinterpret_cast<const float4*>(src + (size_t)ch * 128 + v0 + m);
-            const float4 f = dst[m / 4];
-            acc[m] = f.x; acc[m + 1] = f.y; acc[m + 2] = f.z; acc[m + 3] = f.w;
+        if (threadIdx.x == 0) {
+            mbar_arrive_expect_tx(bar, 65536);
+            bulk_g2s(smem_u32(sm), sg.M + at(g), 65536, bar);
         }
-        __syncthreads();
-        const float* M = sg.M + at;
-#pragma unroll 2
-        for (int c = 0; c < 128; c += 4) {
-            float w[4];
-            if (REVERSE) {
+        float S[64];
+        const float* src = sg.F + at(from) + (size_t)k0 * 128 + v;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = M[(size_t)(c + k) * 128 + ch];
-            } else {
-                const float4 w4 = *reinterpret_cast<const float4*>(M + (size_t)ch * 128 + c);
-                w[0] = w4.x; w[1] = w4.y; w[2] = w4.z; w[3] = w4.w;
+        for (int k = 0; k < 64; ++k) S[k] = src[(size_t)k * 128];
+        float* dst = sg.F + at(g) + (size_t)(16 * warp) * 128 + v;
+        const bool ok = mbar_wait(bar, (uint32_t)i & 1u);
+#pragma unroll 1
+        for (int r = 0; r < 16; r += 4) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const int row = 16 * warp + r;
+#pragma unroll
+            for (int k = 0; k < 64; k += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // four consecutive terms of row row + e, or (reverse) term k + e of rows row .. row + 3
+                    const float4 w = *reinterpret_cast<const float4*>(REVERSE ? sM + (k0 + k + e) * 128 + row
+                                                                              : sM + (row + e) * 128 + k0 + k);
+                    if (REVERSE) {
+                        acc[0] = fmaf(w.x, S[k + e], acc[0]); acc[1] = fmaf(w.y, S[k + e], acc[1]);
+                        acc[2] = fmaf(w.z, S[k + e], acc[2]); acc[3] = fmaf(w.w, S[k + e], acc[3]);
+                    } else {
+                        acc[e] = fmaf(w.x, S[k], acc[e]); acc[e] = fmaf(w.y, S[k + 1], acc[e]);
+                        acc[e] = fmaf(w.z, S[k + 2], acc[e]); acc[e] = fmaf(w.w, S[k + 3], acc[e]);
+                    }
+                }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int m = 0; m < kJoinCols; ++m) acc[m] = fmaf(w[k], sS[c + k][m], acc[m]);
+            for (int e = 0; e < 4; ++e) {
+                acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], 16);
+                if (ok && lane < 16) dst[(size_t)(r + e) * 128] += acc[e];
+            }
         }
-        __syncthreads();
-#pragma unroll
-        for (int m = 0; m < kJoinCols; m += 4) {
-            const float4 f = make_float4(acc[m], acc[m + 1], acc[m + 2], acc[m + 3]);
-            dst[m / 4] = f;
-            *reinterpret_cast<float4*>(&sS[ch][m]) = f;
-        }
+        __syncthreads();  // M consumed, F' visible to the CTA
     }
 }
 
 // Chunks a segment, from the number of chains and their length (for packed sequences the mean; the lengths
-// are on the device).  Modelled in microseconds: a chunk costs 2.9 in the real pass and 2.3 in the ends', the
-// join 4 a segment, and the CTAs of a pass run in waves of one an SM.  Measured at 512 chunks x 32 heads.
+// are on the device).  Modelled in microseconds: a chunk costs 3.1 in the real pass and 2.25 in the ends',
+// the join 4 a segment; past one CTA an SM a pass grows with the CTAs, and by 0.4 for its last, part-filled wave.
+// Measured at 512 chunks x 32 heads: 4 segments 424 + 420 us, 3 segments 385 + 519.
 inline int segment_length(int max_chunks, int N, int H)
 {
     constexpr int kSms = 148, kMaxSeqs = 1024, kMinLen = 4;
     if (N > kMaxSeqs || max_chunks == 0) return 0;
     const long long chains = (long long)N * H;
     const int L = (max_chunks + N - 1) / N;
-    auto waves = [&](long long ctas) { return (double)((ctas + kSms - 1) / kSms); };
-    double best = waves(chains) * L * 2.9;
+    auto waves = [&](long long ctas) { return ctas <= kSms ? 1.0 : (double)ctas / kSms + 0.4; };
+    double best = waves(chains) * L * 3.1;
     int len = 0;
     for (int g = 2; g <= 64 && L / g >= kMinLen; ++g) {
         const int l = (L + g - 1) / g;
-        const double t = waves(chains * g) * l * 2.9 + waves(chains * (2 * g - 3)) * l * 2.3 + 4.0 * (g - 2) + 10.0;
+        const double t = (waves(chains * g) * 3.1 + waves(chains * (2 * g - 3)) * 2.25) * l + 4.0 * (g - 2) + 10.0;
         if (t < 0.95 * best) {
             best = t;
             len = l;
@@ -1047,8 +1061,10 @@ cudaError_t launch_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
 template <bool REVERSE>
 cudaError_t launch_join(const WsHeader* hdr, const int* off, int N, int H, const Segments& sg, cudaStream_t stream)
 {
+    const cudaError_t e = cudaFuncSetAttribute(gdn_join_kernel<REVERSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmem);
+    if (e != cudaSuccess) return e;
     LaunchScope ls("gdn_join", stream);
-    gdn_join_kernel<REVERSE><<<dim3(N, H, 128 / kJoinCols), 128, 0, stream>>>(hdr, off, N, H, sg);
+    gdn_join_kernel<REVERSE><<<dim3(N, H, 128 / kJoinCols), kJoinThreads, kJoinSmem, stream>>>(hdr, off, N, H, sg);
     return cudaGetLastError();
 }
 
