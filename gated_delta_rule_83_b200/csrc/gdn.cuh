@@ -1,6 +1,6 @@
 // gdn.cuh -- the gated delta rule with one forget gate a head, on the CUDA-core chunk kernels.
 //
-// Every configuration the tensor-core kernels do not take (fp32, d = 64) runs here.  The per-channel
+// fp32 inputs run here.  The per-channel
 // kernels hold the scalar gate as the special case of equal channels, so the gate is spread over the
 // dk channels into the workspace, and in the backward the channels' gate gradients are summed.
 #pragma once

@@ -6,8 +6,9 @@ namespace {
 
 bool gdn_heads_ok(int H, int Hk) { return H > 0 && Hk > 0 && H % Hk == 0; }
 
-// bf16 with dk = dv = 128 runs on the tensor cores, everything else on the CUDA-core chunk kernels
-bool gdn_use_tc(kda_dtype dt, int dk, int dv) { return dt == KDA_BF16 && dk == 128 && dv == 128; }
+// bf16 runs on the tensor cores.  fp32 inputs run on the CUDA-core chunk kernels: split into bf16 parts they
+// would lose eight of their bits.
+bool gdn_use_tc(kda_dtype dt) { return dt == KDA_BF16; }
 
 struct GdnFwdPlan {
     Plan f;
@@ -20,7 +21,7 @@ kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, i
 {
     const kda_status st = make_plan(B, T, H, dk, dv, varlen, num_seqs, dt, p.f);
     if (st != KDA_OK) return st;
-    p.tc = gdn_use_tc(dt, dk, dv);
+    p.tc = gdn_use_tc(dt);
     p.gate_bytes = p.tc ? 0 : round_up(sizeof(float) * (size_t)p.f.Ttot * H * dk, kAlign);
     p.total = sizeof(WsHeader) + p.f.off_bytes + p.gate_bytes +
               (p.tc ? gdn::fwd_bytes(p.f.max_chunks, p.f.N, H)
@@ -39,11 +40,11 @@ kda_status make_gdn_bwd_plan(int B, int T, int H, int Hk, int dk, int dv, bool v
 {
     const kda_status st = make_bwd_plan(B, T, H, Hk, 0u, dk, dv, varlen, num_seqs, dt, p.b);
     if (st != KDA_OK) return st;
-    p.tc = gdn_use_tc(dt, dk, dv);
+    p.tc = gdn_use_tc(dt);
     if (p.tc) {
         p.gate_bytes = 0;
         p.total = sizeof(WsHeader) + p.b.f.off_bytes +
-                  gdn::bwd_layout(p.b.f.max_chunks, p.b.f.N, p.b.f.Ttot, H, Hk != H).total;
+                  gdn::bwd_layout(p.b.f.max_chunks, p.b.f.N, p.b.f.Ttot, H, dk, Hk != H).total;
         return KDA_OK;
     }
     p.gate_bytes = round_up(sizeof(float) * (size_t)p.b.f.Ttot * H * dk, kAlign);
@@ -100,17 +101,13 @@ extern "C" kda_status kda_gdn_chunk_fwd(const void* q, const void* k, const void
     cudaError_t e = cudaSuccess;
     if (p.tc) {
         e = gdn::launch_fwd(q, k, v, log_alpha, beta, S0, S_final, out, hdr, off, cu_seqlens, p.f.Tseq, p.f.N, H, Hk,
-                            p.f.max_chunks, p.f.Ttot, (uint8_t*)slots, stream);
+                            dk, dv, p.f.max_chunks, p.f.Ttot, (uint8_t*)slots, stream);
         return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
     if (p.f.Ttot > 0) e = launch_gdn_spread_gate(log_alpha, gate, p.f.Ttot * H, dk, stream);
     if (e == cudaSuccess)
-        e = dt == KDA_BF16 ? launch_simt_prefill<__nv_bfloat16>(q, k, v, gate, beta, S0, S_final, out, hdr, off,
-                                                                cu_seqlens, p.f.Tseq, p.f.N, H, Hk, 0u, dk, dv,
-                                                                p.f.max_chunks, slots, stream)
-                           : launch_simt_prefill<float>(q, k, v, gate, beta, S0, S_final, out, hdr, off, cu_seqlens,
-                                                        p.f.Tseq, p.f.N, H, Hk, 0u, dk, dv, p.f.max_chunks, slots,
-                                                        stream);
+        e = launch_simt_prefill<float>(q, k, v, gate, beta, S0, S_final, out, hdr, off, cu_seqlens, p.f.Tseq, p.f.N, H, Hk,
+                                       0u, dk, dv, p.f.max_chunks, slots, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -157,7 +154,7 @@ extern "C" kda_status kda_gdn_chunk_bwd(const void* q, const void* k, const void
             if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
         }
         const cudaError_t e = gdn::launch_bwd(q, k, v, log_alpha, beta, S0, dout, dS_final, dq, dk_out, dv_out, dlog_alpha,
-                                              dbeta, dS0, hdr, off, cu_seqlens, f.Tseq, f.N, H, Hk, f.max_chunks, Ttot,
+                                              dbeta, dS0, hdr, off, cu_seqlens, f.Tseq, f.N, H, Hk, dk, dv, f.max_chunks, Ttot,
                                               (uint8_t*)(ws + sizeof(WsHeader) + f.off_bytes), stream);
         return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }

@@ -1,4 +1,4 @@
-// gdn_bwd_tc.cuh -- tensor-core backward of the scalar-gate delta rule, bf16, dk = dv = 128.
+// gdn_bwd_tc.cuh -- tensor-core backward of the scalar-gate delta rule, bf16, dk and dv 64 or 128.
 //
 // With the chunk form of gdn_tc.cuh (T = (I + A)^-1, w_j = 2^(g_C - g_j), D_ij = 2^(g_i - g_j)) and the
 // cotangents dO and dS' (of the state after the chunk):
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
 gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_do,
                      const float* __restrict__ dS_final, float* __restrict__ dS0, __nv_bfloat16* __restrict__ dv_out,
                      const WsHeader* __restrict__ hdr, const int* __restrict__ off, const int32_t* __restrict__ cu,
-                     int Tseq, int N, int H, int G, const uint8_t* __restrict__ slots,
+                     int Tseq, int N, int H, int G, int dkw, int dvw, const uint8_t* __restrict__ slots,
                      const uint8_t* __restrict__ bslots, uint8_t* __restrict__ images, Segments sg)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -64,10 +64,12 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     long long s0, s1;
     seq_bounds(n, cu, Tseq, s0, s1);
     s0 += 64LL * seg * sg.len;
-    const float* start = seg == nseg - 1 ? (dS_final ? dS_final + ((size_t)n * H + h) * 16384 : nullptr)
-                                         : ENDS ? nullptr : sg.F + ((size_t)(sidx + 1) * H + h) * 16384;
-    float* end = ENDS ? sg.F + ((size_t)sidx * H + h) * 16384
-                      : dS0 && seg == 0 ? dS0 + ((size_t)n * H + h) * 16384 : nullptr;
+    const size_t mine = ((size_t)n * H + h) * dkw * dvw, part = ((size_t)sidx * H + h) * 16384;
+    const StateRef start = seg == nseg - 1
+                               ? StateRef{dS_final ? const_cast<float*>(dS_final) + mine : nullptr, dvw, dkw, dvw}
+                               : StateRef{ENDS ? nullptr : sg.F + part + (size_t)H * 16384, 128, 128, 128};
+    const StateRef end = ENDS ? StateRef{sg.F + part, 128, 128, 128}
+                              : StateRef{dS0 && seg == 0 ? dS0 + mine : nullptr, dvw, dkw, dvw};
     uint8_t* sm = align1024(smem_raw);
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + kRMisc;
@@ -215,11 +217,8 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const int wg = warp >> 2, d = 32 * (warp & 3) + lane;
         const bool odd = lane & 1;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const size_t srow = (size_t)wg * 64 * 128 + d;
         f32x2 S[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-            S[c] = start ? pair(start[srow + (size_t)(2 * c) * 128], start[srow + (size_t)(2 * c + 1) * 128]) : 0ull;
+        load_state(start, wg, d, S);
         auto put_state = [&](int it) {  // the operand of step `it` and its image, the cotangent after that chunk
             uint32_t hi[32], lo[32];
 #pragma unroll
@@ -301,16 +300,17 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 for (int m = 0; m < 16; ++m) split2(x[2 * m], x[2 * m + 1], hi[m], lo[m]);
                 store_blocks<4>(images + u * kImages + kImgDr, 16384, 4 * wg, d, hi, lo);
                 const long long t = s0 + 64LL * c + 32 * wg;
-                const int Lw = (int)(s1 - t < 32 ? s1 - t : 32);
-                const size_t row = (size_t)H * 128;
-                __nv_bfloat16* o = dv_out + ((size_t)t * H + h) * 128 + (d & ~1) + (odd ? row : 0);
+                const int Lw = !ok || d >= dvw ? 0 : (int)(s1 - t < 32 ? s1 - t : 32) - (odd ? 1 : 0);
+                const size_t row = (size_t)H * dvw;
+                __nv_bfloat16* o = dv_out + ((size_t)t * H + h) * dvw + (d & ~1) + (odd ? row : 0);
 #pragma unroll
                 for (int m = 0; m < 16; ++m) {
                     float a, b;
                     unpair(mul2(be[m], pair(x[2 * m], x[2 * m + 1])), a, b);
                     const uint32_t z = pack_bf16(a, b), got = __shfl_xor_sync(0xffffffffu, z, 1);
                     const uint32_t two = odd ? __byte_perm(got, z, 0x7632) : __byte_perm(z, got, 0x5410);
-                    if (ok && 2 * m + (odd ? 1 : 0) < Lw) *reinterpret_cast<uint32_t*>(o + (size_t)(2 * m) * row) = two;
+                    if (2 * m < Lw) *reinterpret_cast<uint32_t*>(o) = two;
+                    o += 2 * row;
                 }
             }
             ok = ok && mbar_wait_ab(bar_d + 8 * wg, par, s_abort);
@@ -325,15 +325,7 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
             put_state(it + 1);
         }
-        if (end && ok) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                float a, b;
-                unpair(S[c], a, b);
-                end[srow + (size_t)(2 * c) * 128] = a;
-                end[srow + (size_t)(2 * c + 1) * 128] = b;
-            }
-        }
+        if (ok) store_state(end, wg, d, S);
     }
     fence_before_sync();
     __syncthreads();
@@ -367,7 +359,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                      const float* __restrict__ la, const float* __restrict__ beta, __nv_bfloat16* __restrict__ dq,
                      __nv_bfloat16* __restrict__ dk, float* __restrict__ dq_acc, float* __restrict__ dk_acc,
                      float* __restrict__ dla, float* __restrict__ dbeta, const WsHeader* __restrict__ hdr,
-                     const int* __restrict__ off, const int32_t* __restrict__ cu, int Tseq, int N, int H, int G,
+                     const int* __restrict__ off, const int32_t* __restrict__ cu, int Tseq, int N, int H, int G, int dkw,
                      const uint8_t* __restrict__ images)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -582,8 +574,8 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     ok = ok && mbar_wait(bar_m + 16, 0);
     fence_after_sync();
-    const bool row = r < L && ok;
-    const size_t orow = ((size_t)(t0 + r) * H + h) * 128 + c0;
+    const bool row = r < L && c0 < dkw && ok;
+    const size_t orow = ((size_t)(t0 + r) * H + h) * dkw + c0;
     float dot = 0.f;
     {
         float x[32];
@@ -691,7 +683,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 struct BwdLayout {
     size_t slots, bslots, images, segs, seg_bytes, dq, dk, total;
 };
-inline BwdLayout bwd_layout(int max_chunks, int N, long long Ttot, int H, bool grouped)
+inline BwdLayout bwd_layout(int max_chunks, int N, long long Ttot, int H, int dk, bool grouped)
 {
     BwdLayout l;
     const long long units = (long long)max_chunks * H;
@@ -701,7 +693,7 @@ inline BwdLayout bwd_layout(int max_chunks, int N, long long Ttot, int H, bool g
     l.segs = l.images + (size_t)units * kImages;
     l.seg_bytes = segments_bytes(max_chunks, N, H);
     l.dq = l.segs + 3 * l.seg_bytes;
-    const size_t acc = grouped ? (size_t)Ttot * H * 128 * sizeof(float) : 0;
+    const size_t acc = grouped ? (size_t)Ttot * H * dk * sizeof(float) : 0;
     l.dk = l.dq + acc;
     l.total = l.dk + acc;
     return l;
@@ -710,14 +702,14 @@ inline BwdLayout bwd_layout(int max_chunks, int N, long long Ttot, int H, bool g
 inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const float* la, const float* beta,
                               const float* S0, const void* dout, const float* dS_final, void* dq, void* dk, void* dv,
                               float* dla, float* dbeta, float* dS0, const WsHeader* hdr, const int* off,
-                              const int32_t* cu, int Tseq, int N, int H, int Hk, int max_chunks, long long Ttot,
-                              uint8_t* ws, cudaStream_t stream)
+                              const int32_t* cu, int Tseq, int N, int H, int Hk, int dkw, int dvw, int max_chunks,
+                              long long Ttot, uint8_t* ws, cudaStream_t stream)
 {
     alignas(64) CUtensorMap tq{}, tk{}, tv{}, tdo{};
     const long long units = (long long)max_chunks * H;
     if (units > 0x7fffffffLL || ((long long)max_chunks + N) * H > 0x7fffffffLL) return cudaErrorInvalidValue;
     const bool grouped = Hk != H;
-    const BwdLayout lay = bwd_layout(max_chunks, N, Ttot, H, grouped);
+    const BwdLayout lay = bwd_layout(max_chunks, N, Ttot, H, dkw, grouped);
     const int len = Ttot > 0 ? segment_length(max_chunks, N, H) : 0;
     float* segs = (float*)(ws + lay.segs);
     const Segments fwd{len, segs, (float*)((uint8_t*)segs + lay.seg_bytes)};
@@ -726,13 +718,13 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
     float *dq_acc = grouped ? (float*)(ws + lay.dq) : nullptr, *dk_acc = grouped ? (float*)(ws + lay.dk) : nullptr;
     cudaError_t e = cudaSuccess;
     if (Ttot > 0) {
-        if (!make_token_map(&tq, q, true, Hk, Ttot, 64) || !make_token_map(&tk, k, true, Hk, Ttot, 64) ||
-            !make_token_map(&tv, v, true, H, Ttot, 64) || !make_token_map(&tdo, dout, true, H, Ttot, 64))
+        if (!make_map(&tq, q, Hk, dkw, Ttot) || !make_map(&tk, k, Hk, dkw, Ttot) || !make_map(&tv, v, H, dvw, Ttot) ||
+            !make_map(&tdo, dout, H, dvw, Ttot))
             return cudaErrorInvalidValue;
         e = launch_prep<true>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, slots, bslots, stream);
         if (e == cudaSuccess)
-            e = run_chain<kChainStates>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, max_chunks, slots,
-                                        images, fwd, stream);
+            e = run_chain<kChainStates>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, dkw, dvw, max_chunks,
+                                        slots, images, fwd, stream);
         if (e != cudaSuccess) return e;
     }
     e = cudaFuncSetAttribute(gdn_bwd_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRSmem);
@@ -744,7 +736,8 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
         {
             LaunchScope ls("gdn_bwd_ends", stream);
             gdn_bwd_chain_kernel<true><<<grid, kRThreads, kRSmem, stream>>>(
-                tk, tdo, dS_final, nullptr, nullptr, hdr, off, cu, Tseq, N, H, H / Hk, slots, bslots, nullptr, rev);
+                tk, tdo, dS_final, nullptr, nullptr, hdr, off, cu, Tseq, N, H, H / Hk, dkw, dvw, slots, bslots,
+                nullptr, rev);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
         if ((e = launch_join<true>(hdr, off, N, H, rev, stream)) != cudaSuccess) return e;
@@ -752,7 +745,8 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
     {
         LaunchScope ls("gdn_bwd_chain", stream);
         gdn_bwd_chain_kernel<false><<<grid, kRThreads, kRSmem, stream>>>(
-            tk, tdo, dS_final, dS0, (__nv_bfloat16*)dv, hdr, off, cu, Tseq, N, H, H / Hk, slots, bslots, images, rev);
+            tk, tdo, dS_final, dS0, (__nv_bfloat16*)dv, hdr, off, cu, Tseq, N, H, H / Hk, dkw, dvw, slots, bslots,
+            images, rev);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (Ttot == 0) return cudaSuccess;
@@ -762,7 +756,7 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
         LaunchScope ls("gdn_bwd_grads", stream);
         gdn_bwd_grads_kernel<<<(unsigned)units, kGThreads, kGSmem, stream>>>(
             tq, tk, tv, tdo, la, beta, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, dq_acc, dk_acc, dla, dbeta, hdr, off, cu,
-            Tseq, N, H, H / Hk, images);
+            Tseq, N, H, H / Hk, dkw, images);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (grouped) {
@@ -770,9 +764,9 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
         const long long rows = Ttot * Hk, blocks = (rows + kRowWarps - 1) / kRowWarps;
         if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
         bwd_qk_grad_kernel<__nv_bfloat16><<<(unsigned)blocks, 32 * kRowWarps, 0, stream>>>(
-            dq_acc, (const __nv_bfloat16*)q, (__nv_bfloat16*)dq, rows, H / Hk, 128, false);
+            dq_acc, (const __nv_bfloat16*)q, (__nv_bfloat16*)dq, rows, H / Hk, dkw, false);
         bwd_qk_grad_kernel<__nv_bfloat16><<<(unsigned)blocks, 32 * kRowWarps, 0, stream>>>(
-            dk_acc, (const __nv_bfloat16*)k, (__nv_bfloat16*)dk, rows, H / Hk, 128, false);
+            dk_acc, (const __nv_bfloat16*)k, (__nv_bfloat16*)dk, rows, H / Hk, dkw, false);
         e = cudaGetLastError();
     }
     return e;

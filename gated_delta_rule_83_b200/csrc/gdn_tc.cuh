@@ -1,4 +1,7 @@
-// gdn_tc.cuh -- tensor-core (tcgen05 / TMEM) kernels of the scalar-gate delta rule, bf16, dk = dv = 128.
+// gdn_tc.cuh -- tensor-core (tcgen05 / TMEM) kernels of the scalar-gate delta rule, bf16, dk and dv 64 or 128.
+// Tiles are 128 wide; a width of 64 is padded with zeros by the tile loads (which fill what lies outside the
+// tensor) and by masks where states and results enter and leave.
+//
 //
 // Chunk form, 64 tokens a chunk, g_i = sum_{m <= i} log alpha_m inside the chunk (log2 units), C = 64:
 //     A_ij = beta_i 2^(g_i - g_j) k_i.k_j  (j < i)      X = (I + A)^-1 diag(beta)
@@ -474,6 +477,33 @@ struct Segments {
     float* M;         // [segment][H][128][128]
 };
 
+// a state in global memory: [dk][dv] of the caller, or 128 x 128 of the workspace
+struct StateRef {
+    float* p;
+    int stride, rows, cols;
+};
+// channels 64 wg .. + 63 of value column d, as pairs
+__device__ __forceinline__ void load_state(const StateRef& s, int wg, int d, f32x2 (&S)[32])
+{
+    const bool in = s.p && d < s.cols && 64 * wg < s.rows;
+    const float* p = s.p + (size_t)(64 * wg) * s.stride + d;
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        S[c] = in ? pair(p[(size_t)(2 * c) * s.stride], p[(size_t)(2 * c + 1) * s.stride]) : 0ull;
+}
+__device__ __forceinline__ void store_state(const StateRef& s, int wg, int d, const f32x2 (&S)[32])
+{
+    if (!s.p || d >= s.cols || 64 * wg >= s.rows) return;
+    float* p = s.p + (size_t)(64 * wg) * s.stride + d;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        float a, b;
+        unpair(S[c], a, b);
+        p[(size_t)(2 * c) * s.stride] = a;
+        p[(size_t)(2 * c + 1) * s.stride] = b;
+    }
+}
+
 // segment idx -> its sequence, number and the sequence's count; false past the last one (whole warps)
 __device__ __forceinline__ bool find_segment(int idx, const int* __restrict__ off, int N, const Segments& sg, bool varlen,
                                              int& n, int& seg, int& nseg)
@@ -553,8 +583,8 @@ __global__ void __launch_bounds__(Chain<MODE>::kThreads, 1)
 gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const float* S0, float* S_final,
                  __nv_bfloat16* __restrict__ out, const WsHeader* __restrict__ hdr, const int* __restrict__ off,
-                 const int32_t* __restrict__ cu, int Tseq, int N, int H, int G, const uint8_t* __restrict__ slots,
-                 uint8_t* __restrict__ images, Segments sg)
+                 const int32_t* __restrict__ cu, int Tseq, int N, int H, int G, int dkw, int dvw,
+                 const uint8_t* __restrict__ slots, uint8_t* __restrict__ images, Segments sg)
 {
     using C = Chain<MODE>;
     constexpr bool kOut = MODE == kChainOut;
@@ -570,10 +600,11 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     long long s0, s1;
     seq_bounds(n, cu, Tseq, s0, s1);
     s0 += 64LL * seg * sg.len;
-    const float* start = seg == 0 ? (S0 ? S0 + ((size_t)n * H + h) * 16384 : nullptr)
-                                  : MODE == kChainEnds ? nullptr : sg.F + ((size_t)(sidx - 1) * H + h) * 16384;
-    float* end = MODE == kChainEnds ? (trans ? sg.M : sg.F) + ((size_t)sidx * H + h) * 16384
-                                    : S_final && seg == nseg - 1 ? S_final + ((size_t)n * H + h) * 16384 : nullptr;
+    const size_t mine = ((size_t)n * H + h) * dkw * dvw, part = ((size_t)sidx * H + h) * 16384;
+    const StateRef start = seg == 0 ? StateRef{S0 ? const_cast<float*>(S0) + mine : nullptr, dvw, dkw, dvw}
+                                    : StateRef{MODE == kChainEnds ? nullptr : sg.F + part - (size_t)H * 16384, 128, 128, 128};
+    const StateRef end = MODE == kChainEnds ? StateRef{(trans ? sg.M : sg.F) + part, 128, 128, 128}
+                                            : StateRef{S_final && seg == nseg - 1 ? S_final + mine : nullptr, dvw, dkw, dvw};
     uint8_t* sm = align1024(smem_raw);
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + C::Misc;
@@ -801,26 +832,27 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             warp_arrive(bar_q);
             // neighbours exchange: the even lane stores columns (d, d + 1) of the even token, the odd lane of the odd
-            const size_t row = (size_t)H * 128;
-            __nv_bfloat16* o = out + ((size_t)t * H + h) * 128 + (d & ~1) + (odd ? row : 0);
+            const size_t row = (size_t)H * dvw;
+            const int Lo = d < dvw && ok ? L - (odd ? 1 : 0) : 0;
+            __nv_bfloat16* o = out + ((size_t)t * H + h) * dvw + (d & ~1) + (odd ? row : 0);
 #pragma unroll
             for (int m = 0; m < 32; ++m) {
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, z[m], 1);
                 const uint32_t two = odd ? __byte_perm(got, z[m], 0x7632) : __byte_perm(z[m], got, 0x5410);
-                if (ok && 2 * m + (odd ? 1 : 0) < L) *reinterpret_cast<uint32_t*>(o + (size_t)(2 * m) * row) = two;
+                if (2 * m < Lo) *reinterpret_cast<uint32_t*>(o) = two;
+                o += 2 * row;
             }
         }
     } else {
         const int wg = warp >> 2, d = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const size_t srow = (size_t)wg * 64 * 128 + d;
         if (kOut) regs_inc<176>();
         f32x2 S[32];
+        load_state(start, wg, d, S);
+        if (trans) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            const int ch = 64 * wg + 2 * c;
-            S[c] = start ? pair(start[srow + (size_t)(2 * c) * 128], start[srow + (size_t)(2 * c + 1) * 128])
-                         : trans ? pair(ch == d ? 1.f : 0.f, ch + 1 == d ? 1.f : 0.f) : 0ull;
+            for (int c = 0; c < 32; ++c)
+                S[c] = pair(64 * wg + 2 * c == d ? 1.f : 0.f, 64 * wg + 2 * c + 1 == d ? 1.f : 0.f);
         }
         // the state operand of chunk `it`, and for the backward its image
         auto put_state = [&](int it) {
@@ -911,19 +943,24 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             put_state(it + 1);
         }
-        if (end && ok) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                float a, b;
-                unpair(S[c], a, b);
-                end[srow + (size_t)(2 * c) * 128] = a;
-                end[srow + (size_t)(2 * c + 1) * 128] = b;
-            }
-        }
+        if (ok) store_state(end, wg, d, S);
     }
     fence_before_sync();
     __syncthreads();
     if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// [tokens][heads][d] bf16 as a 3-D map of 64-token, 64-channel boxes that land 128B-swizzled
+inline bool make_map(CUtensorMap* m, const void* base, int heads, int d, long long ntok)
+{
+    TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)ntok};
+    const cuuint64_t strides[2] = {2 * (cuuint64_t)d, 2 * (cuuint64_t)d * heads};
+    const cuuint32_t box[3] = {64, 1, 64}, estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool BWD>
@@ -1015,15 +1052,15 @@ gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, i
 
 // Chunks a segment, from the number of chains and their length (for packed sequences the mean; the lengths
 // are on the device).  Modelled in microseconds: a chunk costs 3.1 in the real pass and 2.25 in the ends',
-// the join 4 a segment; past one CTA an SM a pass grows with the CTAs, and by 0.4 for its last, part-filled wave.
-// Measured at 512 chunks x 32 heads: 4 segments 424 + 420 us, 3 segments 385 + 519.
+// the join 4 a segment; past one CTA an SM a pass grows with the CTAs, and by 0.7 for its last, part-filled wave.
+// Measured at 512 chunks x 32 heads: 3 segments 385 + 519 us, 4 segments 510 + 437, none 1520.
 inline int segment_length(int max_chunks, int N, int H)
 {
     constexpr int kSms = 148, kMaxSeqs = 1024, kMinLen = 4;
     if (N > kMaxSeqs || max_chunks == 0) return 0;
     const long long chains = (long long)N * H;
     const int L = (max_chunks + N - 1) / N;
-    auto waves = [&](long long ctas) { return ctas <= kSms ? 1.0 : (double)ctas / kSms + 0.4; };
+    auto waves = [&](long long ctas) { return ctas <= kSms ? 1.0 : (double)ctas / kSms + 0.7; };
     double best = waves(chains) * L * 3.1;
     int len = 0;
     for (int g = 2; g <= 64 && L / g >= kMinLen; ++g) {
@@ -1046,8 +1083,8 @@ inline size_t segments_bytes(int max_chunks, int N, int H)
 template <int MODE>
 cudaError_t launch_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const float* S0,
                          float* S_final, void* out, const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq,
-                         int N, int H, int Hk, int max_chunks, const uint8_t* slots, uint8_t* images, const Segments& sg,
-                         cudaStream_t stream)
+                         int N, int H, int Hk, int dk, int dv, int max_chunks, const uint8_t* slots, uint8_t* images,
+                         const Segments& sg, cudaStream_t stream)
 {
     using C = Chain<MODE>;
     const cudaError_t e = cudaFuncSetAttribute(gdn_chain_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
@@ -1055,7 +1092,7 @@ cudaError_t launch_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
     LaunchScope ls(MODE == kChainOut ? "gdn_chain" : MODE == kChainStates ? "gdn_bwd_states" : "gdn_ends", stream);
     const dim3 grid((unsigned)(max_segments(max_chunks, N, sg.len) * H), MODE == kChainEnds ? 2 : 1);
     gdn_chain_kernel<MODE><<<grid, C::kThreads, C::Smem, stream>>>(tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, hdr, off,
-                                                                  cu, Tseq, N, H, H / Hk, slots, images, sg);
+                                                                  cu, Tseq, N, H, H / Hk, dk, dv, slots, images, sg);
     return cudaGetLastError();
 }
 template <bool REVERSE>
@@ -1072,17 +1109,17 @@ cudaError_t launch_join(const WsHeader* hdr, const int* off, int N, int H, const
 template <int MODE>
 cudaError_t run_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const float* S0,
                       float* S_final, void* out, const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq, int N,
-                      int H, int Hk, int max_chunks, const uint8_t* slots, uint8_t* images, Segments sg,
+                      int H, int Hk, int dk, int dv, int max_chunks, const uint8_t* slots, uint8_t* images, Segments sg,
                       cudaStream_t stream)
 {
     if (sg.len) {
-        cudaError_t e = launch_chain<kChainEnds>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, max_chunks,
-                                                 slots, nullptr, sg, stream);
+        cudaError_t e = launch_chain<kChainEnds>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, dk, dv,
+                                                 max_chunks, slots, nullptr, sg, stream);
         if (e == cudaSuccess) e = launch_join<false>(hdr, off, N, H, sg, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_chain<MODE>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, max_chunks, slots, images, sg,
-                              stream);
+    return launch_chain<MODE>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, dk, dv, max_chunks, slots, images,
+                              sg, stream);
 }
 
 // bytes behind the header and the chunk table
@@ -1093,8 +1130,8 @@ inline size_t fwd_bytes(int max_chunks, int N, int H)
 
 inline cudaError_t launch_fwd(const void* q, const void* k, const void* v, const float* la, const float* beta,
                               const float* S0, float* S_final, void* out, const WsHeader* hdr, const int* off,
-                              const int32_t* cu, int Tseq, int N, int H, int Hk, int max_chunks, long long Ttot,
-                              uint8_t* ws, cudaStream_t stream)
+                              const int32_t* cu, int Tseq, int N, int H, int Hk, int dk, int dv, int max_chunks,
+                              long long Ttot, uint8_t* ws, cudaStream_t stream)
 {
     alignas(64) CUtensorMap tq{}, tk{}, tv{};
     const long long units = (long long)max_chunks * H;
@@ -1103,14 +1140,13 @@ inline cudaError_t launch_fwd(const void* q, const void* k, const void* v, const
     const size_t sb = segments_bytes(max_chunks, N, H);
     const Segments sg{Ttot > 0 ? segment_length(max_chunks, N, H) : 0, (float*)segs, (float*)(segs + sb)};
     if (Ttot > 0) {
-        if (!make_token_map(&tq, q, true, Hk, Ttot, 64) || !make_token_map(&tk, k, true, Hk, Ttot, 64) ||
-            !make_token_map(&tv, v, true, H, Ttot, 64))
+        if (!make_map(&tq, q, Hk, dk, Ttot) || !make_map(&tk, k, Hk, dk, Ttot) || !make_map(&tv, v, H, dv, Ttot))
             return cudaErrorInvalidValue;
         const cudaError_t e = launch_prep<false>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, ws, nullptr, stream);
         if (e != cudaSuccess) return e;
     }
-    return run_chain<kChainOut>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, max_chunks, ws, nullptr, sg,
-                                stream);
+    return run_chain<kChainOut>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, dk, dv, max_chunks, ws, nullptr,
+                                sg, stream);
 }
 
 }  // namespace gdn

@@ -122,6 +122,10 @@ SHAPES = [
     ("bf16", 2, 1, 128, 128, dict(T=300, gate=0.0)),
     ("bf16", 2, 2, 128, 128, dict(T=300, gate=9.0)),
     ("bf16", 2, 2, 128, 128, dict(T=260, corr=0.3)),
+    ("bf16", 1, 1, 128, 128, dict(lens=[700, 0, 1333, 64, 1, 2100])),
+    ("bf16", 2, 1, 64, 128, dict(lens=[900, 30, 1500])),
+    ("bf16", 3, 3, 128, 64, dict(T=2065)),
+    ("bf16", 2, 2, 64, 64, dict(T=700, B=2, s0=False)),
     ("fp32", 2, 2, 128, 128, dict(T=200)),
     ("fp32", 2, 1, 64, 64, dict(T=256)),
     ("fp32", 2, 2, 64, 128, dict(lens=[70, 0, 1, 128])),
