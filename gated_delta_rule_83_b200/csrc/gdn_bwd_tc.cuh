@@ -255,20 +255,12 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             const uint32_t par = (uint32_t)it & 1u, sc = sb + s * kRStage + kRScal;
             const size_t u = (size_t)(jb + c) * H + h;
             ok = ok && mbar_wait_ab(bar_full + 8 * s, (uint32_t)(it >> 1) & 1u, s_abort);
-            f32x2 w[16], be[16], nbg[16];
+            f32x2 w[16];  // token rows of the scalars are fetched ahead of each use, while an MMA runs
 #pragma unroll
-            for (int m = 0; m < 16; m += 2) {
-                lds_pairs(sc + 4 * (kW + 32 * wg + 2 * m), w[m], w[m + 1]);
-                lds_pairs(sc + 4 * (kBeta + 32 * wg + 2 * m), be[m], be[m + 1]);
-                lds_pairs(sc + 4 * (kNgam + 32 * wg + 2 * m), nbg[m], nbg[m + 1]);
-            }
-#pragma unroll
-            for (int m = 0; m < 16; ++m) nbg[m] = mul2(nbg[m], be[m]);
+            for (int m = 0; m < 16; m += 2) lds_pairs(sc + 4 * (kW + 32 * wg + 2 * m), w[m], w[m + 1]);
             float last1;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(last1) : "r"(sc + 4 * (kGam + 63)));
             const f32x2 last = pair(last1, last1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
             float x[32];
             f32x2 y[16];
             {
@@ -285,12 +277,23 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             tmem_put_split32(tl + 32 * wg, y);
             tmem_wait_st();
             warp_arrive(bar_r);
+            f32x2 be[16];
+#pragma unroll
+            for (int m = 0; m < 16; m += 2) {
+                lds_pairs(sc + 4 * (kBeta + 32 * wg + 2 * m), be[m], be[m + 1]);
+                lds_pairs(sc + 4 * (kNgam + 32 * wg + 2 * m), w[m], w[m + 1]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
             ok = ok && mbar_wait_ab(bar_u, par, s_abort);
             fence_after_sync();
             tmem_ld32(tl + 128 + 32 * wg, x);
 #pragma unroll
-            for (int m = 0; m < 16; ++m) y[m] = mul2(nbg[m], pair(x[2 * m], x[2 * m + 1]));
-            tmem_put_split32(tl + 128 + 32 * wg, y);
+            for (int m = 0; m < 16; ++m) {
+                y[m] = mul2(be[m], pair(x[2 * m], x[2 * m + 1]));  // dv
+                w[m] = mul2(w[m], y[m]);
+            }
+            tmem_put_split32(tl + 128 + 32 * wg, w);
             tmem_wait_st();
             warp_arrive(bar_w);
             if (it + 1 < nch) clear_tail(it + 1);
@@ -306,7 +309,7 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
                 for (int m = 0; m < 16; ++m) {
                     float a, b;
-                    unpair(mul2(be[m], pair(x[2 * m], x[2 * m + 1])), a, b);
+                    unpair(y[m], a, b);
                     const uint32_t z = pack_bf16(a, b), got = __shfl_xor_sync(0xffffffffu, z, 1);
                     const uint32_t two = odd ? __byte_perm(got, z, 0x7632) : __byte_perm(z, got, 0x5410);
                     if (2 * m < Lw) *reinterpret_cast<uint32_t*>(o) = two;
@@ -375,16 +378,20 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     float* s_red = s_g + 128;                             // [4 sums][4 parts][64 rows]
     float* s_sds = s_red + 1024;                          // [8]
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + kGMisc + 6144);
-    const uint32_t bar_in = sb + kGMisc + 6160, bar_ds = bar_in + 8, bar_m = bar_in + 16;  // 4 MMA barriers
+    const uint32_t bar_in = sb + kGMisc + 6160, bar_s = bar_in + 8, bar_ds = bar_in + 16, bar_read = bar_in + 24,
+                   bar_m = bar_in + 32;  // 4 MMA barriers
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
     const uint8_t* img = images + (size_t)blockIdx.x * kImages;
 
     if (tid == 0) {
         mbar_init(bar_in, 1);
+        mbar_init(bar_s, 1);
         mbar_init(bar_ds, 1);
+        mbar_init(bar_read, 8);
         for (int i = 0; i < 4; ++i) mbar_init(bar_m + 8 * i, 1);
         mbar_fence_init();
-        mbar_arrive_expect_tx(bar_in, kGMisc);
+        mbar_arrive_expect_tx(bar_in, kGMisc - 65536);
+        mbar_arrive_expect_tx(bar_s, 65536);
         for (int a = 0; a < 2; ++a) {
             tma_load_3d(sb + kGDo + 8192 * a, &tm_do, 64 * a, h, (int)t0, bar_in);
             tma_load_3d(sb + kGV + 8192 * a, &tm_v, 64 * a, h, (int)t0, bar_in);
@@ -392,7 +399,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             tma_load_3d(sb + kGQ + 8192 * a, &tm_q, 64 * a, h / G, (int)t0, bar_in);
         }
         bulk_g2s(sb + kGU, img + kImgU, 65536, bar_in);  // U and dR
-        bulk_g2s(sb + kGS, img + kImgS, 65536, bar_in);
+        bulk_g2s(sb + kGS, img + kImgS, 65536, bar_s);
     }
     if (warp == 1) load_scalars(la, beta, t0, L, H, h, s_g, s_b);
     if (warp == 2) {
@@ -422,9 +429,8 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const uint64_t kDo = desc_kmajor(sb + kGDo, 64, 0), kK = desc_kmajor(sb + kGK, 64, 0),
                            kV = desc_kmajor(sb + kGV, 64, 0);
             const uint32_t kn64 = idesc_bf16(64, 64, false, true), mn64 = idesc_bf16(64, 64, true, true),
-                           kk64 = idesc_bf16(64, 64, false, false), kn128 = idesc_bf16(64, 128, false, true),
-                           mn128 = idesc_bf16(64, 128, true, true);
-            constexpr uint64_t loU = 16384 >> 4, loS = 32768 >> 4;
+                           kk64 = idesc_bf16(64, 64, false, false);
+            constexpr uint64_t loU = 16384 >> 4;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const uint64_t km = (uint64_t)(((k >> 2) * 8192 + (k & 3) * 32) >> 4), im = (uint64_t)((k * 256) >> 4);
@@ -438,6 +444,13 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 mma_bf16(tmem + 448, kV + km, iR + loU + im, kn64, 1);
             }
             mma_commit(bar_m);
+        }
+        __syncwarp();
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_s, 0));
+        if (ok && elect_one()) {
+            const uint64_t kDo = desc_kmajor(sb + kGDo, 64, 0);
+            const uint32_t kn128 = idesc_bf16(64, 128, false, true), mn128 = idesc_bf16(64, 128, true, true);
+            constexpr uint64_t loU = 16384 >> 4, loS = 32768 >> 4;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const uint64_t km = (uint64_t)(((k >> 2) * 8192 + (k & 3) * 32) >> 4), im = (uint64_t)((k * 256) >> 4);
@@ -457,6 +470,15 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const int c0 = 64 * (lane >> 4) + 32 * hw;   // this thread's channels
     const int j0 = 32 * (lane >> 4) + 16 * hw;   // its columns of the 64 x 64 products
     const float gi = s_g[r], bi = s_b[r], gam = ex2_approx(gi), wi = ex2_approx(s_g[63] - gi);
+    uint4 sh[8], sl[8];  // this thread's share of S for <S, dS'>, before dS' takes its place
+    ok = ok && mbar_wait(bar_s, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        sh[i] = *reinterpret_cast<const uint4*>(sm + kGS + (tid + 256 * i) * 16);
+        sl[i] = *reinterpret_cast<const uint4*>(sm + kGS + 32768 + (tid + 256 * i) * 16);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_read);
     uint32_t pdh[8], pdl[8], gh[8], gl[8];
     float db = 0.f;
     ok = ok && mbar_wait(bar_m, 0);
@@ -486,9 +508,16 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     float rq[32], ra[32];
     float kt = 0.f;
-    uint4 sh[8], sl[8];  // this thread's share of S for <S, dS'>
     ok = ok && mbar_wait(bar_m + 8, 0);
     fence_after_sync();
+    if (warp == 0) {  // S is consumed
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_read, 0));
+        if (ok && elect_one()) {
+            mbar_arrive_expect_tx(bar_ds, 65536);
+            bulk_g2s(sb + kGS, img + kImgDs, 65536, bar_ds);
+        }
+        __syncwarp();
+    }
     grad_ld32(tl + 32 * hw, rq);
     grad_ld32(tl + 128 + 32 * hw, ra);
 #pragma unroll
@@ -505,11 +534,6 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     db -= gam * kt;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        sh[i] = *reinterpret_cast<const uint4*>(sm + kGS + (tid + 256 * i) * 16);
-        sl[i] = *reinterpret_cast<const uint4*>(sm + kGS + 32768 + (tid + 256 * i) * 16);
-    }
-#pragma unroll
     for (int b = 0; b < 2; ++b) {
         const uint32_t o = sw128_chunk_off(r, (j0 >> 3) + b, 64);
         *reinterpret_cast<uint4*>(sm + kGPd + o) = make_uint4(pdh[4 * b], pdh[4 * b + 1], pdh[4 * b + 2], pdh[4 * b + 3]);
@@ -523,8 +547,6 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     if (warp == 0) {
         fence_after_sync();
         if (ok && elect_one()) {
-            mbar_arrive_expect_tx(bar_ds, 65536);
-            bulk_g2s(sb + kGS, img + kImgDs, 65536, bar_ds);
             const uint64_t kP = desc_kmajor(sb + kGPd, 64, 0), kG = desc_kmajor(sb + kGG, 64, 0),
                            mP = desc_mnmajor(sb + kGPd, 64, 0), mG = desc_mnmajor(sb + kGG, 64, 0),
                            mK = desc_mnmajor(sb + kGK, 64, 0), mQ = desc_mnmajor(sb + kGQ, 64, 0);
