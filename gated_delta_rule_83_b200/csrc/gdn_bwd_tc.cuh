@@ -16,7 +16,6 @@
 // their digits.  Splits and accuracy as in the forward: 4..7e-6 for every fp32 gradient.
 #pragma once
 
-#include "backward_simt.cuh"
 #include "gdn_tc.cuh"
 
 namespace kda {
@@ -700,6 +699,24 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
 }
 
+// dq and dk of a q/k head from its G value heads, in head order: rows of 4 * w channels, 16 bytes a thread
+__global__ void __launch_bounds__(256)
+gdn_bwd_heads_kernel(const float* __restrict__ dq_acc, const float* __restrict__ dk_acc, __nv_bfloat16* __restrict__ dq,
+                     __nv_bfloat16* __restrict__ dk, long long quads, int G, int w)
+{
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= quads) return;
+    const long long row = i / w;
+    const int c = (int)(i - row * w);
+    const float4* acc = reinterpret_cast<const float4*>(blockIdx.y ? dk_acc : dq_acc) + row * G * w + c;
+    float4 s = __ldcs(acc);
+    for (int g = 1; g < G; ++g) {
+        const float4 x = __ldcs(acc + (size_t)g * w);
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    reinterpret_cast<uint2*>(blockIdx.y ? dk : dq)[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
 // bytes behind the header and the chunk table: slots, backward slots, images, segment states (forward,
 // transition, reverse), and with shared q/k heads fp32 dq, dk
 struct BwdLayout {
@@ -783,12 +800,10 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
     }
     if (grouped) {
         LaunchScope ls("gdn_bwd_heads", stream);
-        const long long rows = Ttot * Hk, blocks = (rows + kRowWarps - 1) / kRowWarps;
+        const long long quads = Ttot * Hk * (dkw / 4), blocks = (quads + 255) / 256;
         if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-        bwd_qk_grad_kernel<__nv_bfloat16><<<(unsigned)blocks, 32 * kRowWarps, 0, stream>>>(
-            dq_acc, (const __nv_bfloat16*)q, (__nv_bfloat16*)dq, rows, H / Hk, dkw, false);
-        bwd_qk_grad_kernel<__nv_bfloat16><<<(unsigned)blocks, 32 * kRowWarps, 0, stream>>>(
-            dk_acc, (const __nv_bfloat16*)k, (__nv_bfloat16*)dk, rows, H / Hk, dkw, false);
+        gdn_bwd_heads_kernel<<<dim3((unsigned)blocks, 2), 256, 0, stream>>>(
+            dq_acc, dk_acc, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, quads, H / Hk, dkw / 4);
         e = cudaGetLastError();
     }
     return e;
