@@ -90,7 +90,7 @@ extern "C" kda_status kda_gdn_chunk_fwd(const void* q, const void* k, const void
     char* ws = (char*)workspace;
     WsHeader* hdr = (WsHeader*)ws;
     int* off = (int*)(ws + sizeof(WsHeader));
-    {
+    if (!p.tc || cu_seqlens) {  // the tensor-core kernels derive a regular batch's chunks themselves
         LaunchScope ls("chunk_table", stream);
         chunk_table_kernel<<<1, kTableThreads, 0, stream>>>(cu_seqlens, p.f.N, p.f.Tseq, p.f.Ttot, hdr, off,
                                                             off + p.f.N + 1);
@@ -148,7 +148,7 @@ extern "C" kda_status kda_gdn_chunk_bwd(const void* q, const void* k, const void
         char* ws = (char*)workspace;
         WsHeader* hdr = (WsHeader*)ws;
         int* off = (int*)(ws + sizeof(WsHeader));
-        {
+        if (cu_seqlens) {
             LaunchScope ls("chunk_table", stream);
             chunk_table_kernel<<<1, kTableThreads, 0, stream>>>(cu_seqlens, f.N, f.Tseq, f.Ttot, hdr, off, off + f.N + 1);
             if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
@@ -196,10 +196,11 @@ kda_status check_cache_args(const void* S, const void* cache, const void* scale,
 {
     if (N < 0 || num_slots < 0 || H <= 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID_ARG;
     if (!dims_supported(dk, dv)) return KDA_ERR_UNSUPPORTED;
-    if ((long long)H * dk > 65535LL * 32) return KDA_ERR_UNSUPPORTED;  // the grid's second axis
+    if (H > 65535 || (long long)N * H * dk > (1LL << 32)) return KDA_ERR_UNSUPPORTED;  // rows of a launch
     if (N == 0) return KDA_OK;
     if (!S || !slots || (num_slots > 0 && (!cache || !scale))) return KDA_ERR_INVALID_ARG;
-    if (!all_aligned16({S, cache}) || ((uintptr_t)scale & 3u) || ((uintptr_t)slots & 3u)) return KDA_ERR_INVALID_ARG;
+    if (((uintptr_t)S & 31u) || ((uintptr_t)cache & 15u) || ((uintptr_t)scale & 3u) || ((uintptr_t)slots & 3u))
+        return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
 

@@ -54,12 +54,12 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                      const uint8_t* __restrict__ bslots, uint8_t* __restrict__ images, Segments sg)
 {
     extern __shared__ uint8_t smem_raw[];
-    if (hdr->bad) return;
+    if (cu && hdr->bad) return;
     const int sidx = blockIdx.x / H, h = blockIdx.x - sidx * H;
     int n, seg, nseg;
-    if (!find_segment(sidx, off, N, sg, cu != nullptr, n, seg, nseg)) return;
+    if (!find_segment(sidx, off, cu, Tseq, N, sg, n, seg, nseg)) return;
     if (ENDS && seg == 0) return;  // nothing ends at the first segment's start
-    const int jb = off[n] + seg * sg.len, left = off[n + 1] - jb, nch = seg == nseg - 1 ? left : sg.len;
+    const int jb = chunks_before(off, cu, Tseq, n) + seg * sg.len, left = chunks_before(off, cu, Tseq, n + 1) - jb, nch = seg == nseg - 1 ? left : sg.len;
     long long s0, s1;
     seq_bounds(n, cu, Tseq, s0, s1);
     s0 += 64LL * seg * sg.len;
@@ -365,8 +365,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                      const uint8_t* __restrict__ images)
 {
     extern __shared__ uint8_t smem_raw[];
-    if (hdr->bad) return;
-    if ((long long)blockIdx.x >= (long long)hdr->total_chunks * H) return;
+    if (cu && (hdr->bad || (long long)blockIdx.x >= (long long)hdr->total_chunks * H)) return;
     int h, n, L;
     long long t0;
     tc_unit(blockIdx.x, H, off, cu, Tseq, N, h, n, t0, L);
@@ -779,7 +778,7 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
                 nullptr, rev);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
-        if ((e = launch_join<true>(hdr, off, N, H, rev, stream)) != cudaSuccess) return e;
+        if ((e = launch_join<true>(hdr, off, cu, Tseq, N, H, rev, stream)) != cudaSuccess) return e;
     }
     {
         LaunchScope ls("gdn_bwd_chain", stream);

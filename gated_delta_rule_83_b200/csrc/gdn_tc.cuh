@@ -274,8 +274,7 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 uint8_t* __restrict__ slots, uint8_t* __restrict__ bslots)
 {
     extern __shared__ uint8_t smem_raw[];
-    if (hdr->bad) return;
-    if ((long long)blockIdx.x >= (long long)hdr->total_chunks * H) return;
+    if (cu && (hdr->bad || (long long)blockIdx.x >= (long long)hdr->total_chunks * H)) return;
     int h, n, L;
     long long t0;
     tc_unit(blockIdx.x, H, off, cu, Tseq, N, h, n, t0, L);
@@ -504,18 +503,24 @@ __device__ __forceinline__ void store_state(const StateRef& s, int wg, int d, co
     }
 }
 
+// chunks of the sequences before n; only packed input has a table
+__device__ __forceinline__ int chunks_before(const int* __restrict__ off, const int32_t* cu, int Tseq, int n)
+{
+    return cu ? off[n] : n * ((Tseq + kChunk - 1) / kChunk);
+}
+
 // segment idx -> its sequence, number and the sequence's count; false past the last one (whole warps)
-__device__ __forceinline__ bool find_segment(int idx, const int* __restrict__ off, int N, const Segments& sg, bool varlen,
-                                             int& n, int& seg, int& nseg)
+__device__ __forceinline__ bool find_segment(int idx, const int* __restrict__ off, const int32_t* cu, int Tseq, int N,
+                                             const Segments& sg, int& n, int& seg, int& nseg)
 {
     if (sg.len == 0) {
-        n = off[N + 1 + idx];
+        n = cu ? off[N + 1 + idx] : idx;
         seg = 0;
         nseg = 1;
         return true;
     }
-    if (!varlen) {
-        nseg = max(1, (off[1] - off[0] + sg.len - 1) / sg.len);
+    if (!cu) {
+        nseg = max(1, (chunks_before(off, cu, Tseq, 1) + sg.len - 1) / sg.len);
         n = idx / nseg;
         seg = idx - n * nseg;
         return n < N;
@@ -589,14 +594,14 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     using C = Chain<MODE>;
     constexpr bool kOut = MODE == kChainOut;
     extern __shared__ uint8_t smem_raw[];
-    if (hdr->bad) return;
+    if (cu && hdr->bad) return;
     const int sidx = blockIdx.x / H, h = blockIdx.x - sidx * H;
     const bool trans = MODE == kChainEnds && blockIdx.y == 1;  // from the identity, without v
     int n, seg, nseg;
-    if (!find_segment(sidx, off, N, sg, cu != nullptr, n, seg, nseg)) return;
+    if (!find_segment(sidx, off, cu, Tseq, N, sg, n, seg, nseg)) return;
     // nothing starts from the last segment's end, and the first one's start is known
     if (MODE == kChainEnds && (seg == nseg - 1 || (trans && seg == 0))) return;
-    const int jb = off[n] + seg * sg.len, left = off[n + 1] - jb, nch = seg == nseg - 1 ? left : sg.len;
+    const int jb = chunks_before(off, cu, Tseq, n) + seg * sg.len, left = chunks_before(off, cu, Tseq, n + 1) - jb, nch = seg == nseg - 1 ? left : sg.len;
     long long s0, s1;
     seq_bounds(n, cu, Tseq, s0, s1);
     s0 += 64LL * seg * sg.len;
@@ -984,12 +989,13 @@ constexpr int kJoinCols = 16, kJoinThreads = 256;
 constexpr uint32_t kJoinSmem = 65536 + 1024;
 template <bool REVERSE>
 __global__ void __launch_bounds__(kJoinThreads)
-gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, int N, int H, Segments sg)
+gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, const int32_t* __restrict__ cu, int Tseq,
+                int H, Segments sg)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_first;
     __shared__ __align__(8) uint64_t s_bar;
-    if (hdr->bad) return;
+    if (cu && hdr->bad) return;
     const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int v = blockIdx.z * kJoinCols + (lane & 15), k0 = 64 * (lane >> 4);
     uint8_t* sm = align1024(smem_raw);
@@ -997,7 +1003,10 @@ gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, i
     const uint32_t bar = smem_u32(&s_bar);
     // the sequence's first segment: the segments of those before it
     int part = 0;
-    for (int m = threadIdx.x; m < n; m += kJoinThreads) part += max(1, (off[m + 1] - off[m] + sg.len - 1) / sg.len);
+    auto segments = [&](int m) {
+        return (chunks_before(off, cu, Tseq, m + 1) - chunks_before(off, cu, Tseq, m) + sg.len - 1) / sg.len;
+    };
+    for (int m = threadIdx.x; m < n; m += kJoinThreads) part += max(1, segments(m));
     if (threadIdx.x == 0) {
         s_first = 0;
         mbar_init(bar, 1);
@@ -1006,7 +1015,7 @@ gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, i
     __syncthreads();
     if (part) atomicAdd(&s_first, part);
     __syncthreads();
-    const int first = s_first, nseg = (off[n + 1] - off[n] + sg.len - 1) / sg.len;
+    const int first = s_first, nseg = segments(n);
     auto at = [&](int g) { return ((size_t)(first + g) * H + h) * 16384; };
     for (int i = 0; i + 2 < nseg; ++i) {
         const int g = REVERSE ? nseg - 2 - i : 1 + i, from = REVERSE ? g + 1 : g - 1;
@@ -1096,12 +1105,13 @@ cudaError_t launch_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
     return cudaGetLastError();
 }
 template <bool REVERSE>
-cudaError_t launch_join(const WsHeader* hdr, const int* off, int N, int H, const Segments& sg, cudaStream_t stream)
+cudaError_t launch_join(const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq, int N, int H, const Segments& sg,
+                        cudaStream_t stream)
 {
     const cudaError_t e = cudaFuncSetAttribute(gdn_join_kernel<REVERSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmem);
     if (e != cudaSuccess) return e;
     LaunchScope ls("gdn_join", stream);
-    gdn_join_kernel<REVERSE><<<dim3(N, H, 128 / kJoinCols), kJoinThreads, kJoinSmem, stream>>>(hdr, off, N, H, sg);
+    gdn_join_kernel<REVERSE><<<dim3(N, H, 128 / kJoinCols), kJoinThreads, kJoinSmem, stream>>>(hdr, off, cu, Tseq, H, sg);
     return cudaGetLastError();
 }
 
@@ -1115,7 +1125,7 @@ cudaError_t run_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
     if (sg.len) {
         cudaError_t e = launch_chain<kChainEnds>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, dk, dv,
                                                  max_chunks, slots, nullptr, sg, stream);
-        if (e == cudaSuccess) e = launch_join<false>(hdr, off, N, H, sg, stream);
+        if (e == cudaSuccess) e = launch_join<false>(hdr, off, cu, Tseq, N, H, sg, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_chain<MODE>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, dk, dv, max_chunks, slots, images,

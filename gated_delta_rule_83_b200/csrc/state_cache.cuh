@@ -7,9 +7,9 @@
 // 8-bit float: under a row's own scale a uniform step is off by at most max/254, an e4m3 mantissa by up
 // to 1/16 of each large value.  Read: value = code * scale.
 //
-// Both are one streaming pass: 4 + 1 bytes an element.  A thread moves 4 consecutive values of a row
-// (16 B fp32, 4 B codes), so every warp-wide access is a run of whole 128-byte lines, and holds 8 rows
-// in flight at once to cover the memory latency.
+// Both are one streaming pass: 4 + 1 bytes an element.  A thread moves 8 consecutive values of a row (one
+// 32-byte access to the fp32 side, 8 bytes of codes) and holds kCacheRows rows in flight to cover the memory
+// latency; the state's loads are issued before the slot is known.
 #pragma once
 
 #include "common.cuh"
@@ -18,97 +18,131 @@
 namespace kda {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 8;  // rows in flight per thread
+constexpr int kCacheRows = 2;  // rows in flight per thread
 
-// DV / 4 lanes own a row; a block covers kCacheRows * kCacheThreads * 4 / DV rows of one (state, head).
-template <int DV> __host__ __device__ constexpr int cache_block_rows() { return kCacheRows * kCacheThreads * 4 / DV; }
+// DV / 8 lanes own a row; a block covers so many rows of one state
+template <int DV> __host__ __device__ constexpr int cache_block_rows() { return kCacheRows * kCacheThreads * 8 / DV; }
 
-// whether a later entry of `slots` names the same slot: the later one is kept
-__device__ __forceinline__ bool slot_superseded(const int32_t* __restrict__ slots, int n, int N, int slot)
+struct Float8 {
+    float v[8];
+};
+__device__ __forceinline__ Float8 ld_stream8(const float* p)
 {
-    bool later = false;
-    for (int m = n + 1 + (int)threadIdx.x; m < N; m += kCacheThreads) later |= slots[m] == slot;
-    return __syncthreads_or(later) != 0;
+    Float8 x;
+    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(x.v[0]), "=f"(x.v[1]), "=f"(x.v[2]), "=f"(x.v[3]), "=f"(x.v[4]), "=f"(x.v[5]), "=f"(x.v[6]),
+                   "=f"(x.v[7])
+                 : "l"(p));
+    return x;
+}
+__device__ __forceinline__ void st_stream8(float* p, const Float8& x)
+{
+    asm volatile("st.global.L1::no_allocate.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(x.v[0]), "f"(x.v[1]),
+                 "f"(x.v[2]), "f"(x.v[3]), "f"(x.v[4]), "f"(x.v[5]), "f"(x.v[6]), "f"(x.v[7])
+                 : "memory");
 }
 
 template <int DV>
 __global__ void __launch_bounds__(kCacheThreads)
 state_cache_write_kernel(const float* __restrict__ S, int8_t* __restrict__ cache, float* __restrict__ scale,
-                         const int32_t* __restrict__ slots, int N, int num_slots, int rows)
+                         const int32_t* __restrict__ slots, int N, int num_slots, int rows, int blocks)
 {
-    const int n = blockIdx.x;
-    const int slot = slots[n];
+    const int n = blockIdx.x / blocks, block = blockIdx.x % blocks;
+    constexpr int LPR = DV / 8, RPB = kCacheThreads / LPR;  // lanes per row, rows per block pass
+    const int lane = threadIdx.x % LPR;
+    const int r0 = block * cache_block_rows<DV>() + threadIdx.x / LPR;
+    // the slot, the entries behind it and the values are all under way before the first is looked at
+    const int slot = slots[n], m0 = n + 1 + (int)threadIdx.x, behind = m0 < N ? slots[m0] : -1;
+    Float8 x[kCacheRows];
+#pragma unroll
+    for (int i = 0; i < kCacheRows; ++i) {
+        const int r = r0 + i * RPB;
+        if (r < rows) x[i] = ld_stream8(S + ((size_t)n * rows + r) * DV + 8 * lane);
+    }
     if (slot < 0) return;
     if (slot >= num_slots) {
         if (threadIdx.x == 0) set_error(KDA_ERR_INVALID_ARG);
         return;
     }
-    if (slot_superseded(slots, n, N, slot)) return;
-    constexpr int LPR = DV / 4, RPB = kCacheThreads / LPR;  // lanes per row, rows per block pass
-    const int lane = threadIdx.x % LPR;
-    const int r0 = blockIdx.y * cache_block_rows<DV>() + threadIdx.x / LPR;
-    const unsigned members = LPR == 32 ? 0xffffffffu : (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
-    float4 x[kCacheRows];
+    // a later entry names the same slot: that one is kept
+    bool later = behind == slot;
+    for (int m = m0 + kCacheThreads; m < N; m += kCacheThreads) later |= slots[m] == slot;
+    if (__syncthreads_or(later)) return;
+    // the lanes of this thread's row
+    const unsigned members = LPR == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
         const int r = r0 + i * RPB;
-        x[i] = r < rows ? __ldcs(reinterpret_cast<const float4*>(S + ((size_t)n * rows + r) * DV) + lane)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < kCacheRows; ++i) {
-        const int r = r0 + i * RPB;
+        if (r >= rows) break;
         // |x| as an integer: ordered like the value, infinities above every number, NaN above those
-        unsigned m = max(max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu),
-                         max(__float_as_uint(x[i].z) & 0x7fffffffu, __float_as_uint(x[i].w) & 0x7fffffffu));
+        unsigned m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[i].v[e]) & 0x7fffffffu);
         m = __reduce_max_sync(members, m);
         const bool finite = m < 0x7f800000u;
         const float sc = finite ? __fdiv_rn(__uint_as_float(m), 127.f) : __uint_as_float(0x7fc00000u);
-        char4 c = make_char4(0, 0, 0, 0);
+        uint32_t c[2] = {0u, 0u};
         if (finite && sc > 0.f) {  // a denormal scale can leave a quotient above 127: clamped
-            c.x = (signed char)fminf(fmaxf(rintf(__fdiv_rn(x[i].x, sc)), -127.f), 127.f);
-            c.y = (signed char)fminf(fmaxf(rintf(__fdiv_rn(x[i].y, sc)), -127.f), 127.f);
-            c.z = (signed char)fminf(fmaxf(rintf(__fdiv_rn(x[i].z, sc)), -127.f), 127.f);
-            c.w = (signed char)fminf(fmaxf(rintf(__fdiv_rn(x[i].w, sc)), -127.f), 127.f);
+            // The product with the reciprocal is within 127 * 3 * 2^-24 = 2.3e-5 of the quotient, so both round to
+            // the same integer unless it is that near a half; only there (or where the reciprocal overflows)
+            // the division itself is made.  Rounding by adding 1.5 * 2^23, whose last bits then hold the integer:
+            // conversions run at a quarter of the adds' rate.  (Divisions and conversions: 45 us for 64 states of
+            // 32 heads.)
+            constexpr float kMagic = 12582912.f;
+            const float inv = __frcp_rn(sc);
+            uint32_t k[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = x[i].v[e] * inv;
+                float m2 = fminf(fmaxf(y, -127.f), 127.f) + kMagic;
+                if (!(fabsf(y - (m2 - kMagic)) < 0.4999f))
+                    m2 = fminf(fmaxf(__fdiv_rn(x[i].v[e], sc), -127.f), 127.f) + kMagic;
+                k[e] = __float_as_uint(m2);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+                c[e >> 2] = __byte_perm(__byte_perm(k[e], k[e + 1], 0x0040), __byte_perm(k[e + 2], k[e + 3], 0x0040), 0x5410);
         }
-        if (r < rows) {
-            const size_t row = (size_t)slot * rows + r;
-            reinterpret_cast<char4*>(cache + row * DV)[lane] = c;
-            if (lane == 0) scale[row] = sc;
-        }
+        const size_t row = (size_t)slot * rows + r;
+        reinterpret_cast<uint2*>(cache + row * DV)[lane] = make_uint2(c[0], c[1]);
+        if (lane == 0) scale[row] = sc;
     }
 }
 
 template <int DV>
 __global__ void __launch_bounds__(kCacheThreads)
 state_cache_read_kernel(const int8_t* __restrict__ cache, const float* __restrict__ scale,
-                        const int32_t* __restrict__ slots, float* __restrict__ S, int num_slots, int rows)
+                        const int32_t* __restrict__ slots, float* __restrict__ S, int num_slots, int rows, int blocks)
 {
-    const int n = blockIdx.x;
+    const int n = blockIdx.x / blocks, block = blockIdx.x % blocks;
     const int slot = slots[n];
     const bool there = slot >= 0 && slot < num_slots;  // no slot: the zero state of a new sequence
     if (slot >= num_slots && threadIdx.x == 0) set_error(KDA_ERR_INVALID_ARG);
-    constexpr int LPR = DV / 4, RPB = kCacheThreads / LPR;
+    constexpr int LPR = DV / 8, RPB = kCacheThreads / LPR;
     const int lane = threadIdx.x % LPR;
-    const int r0 = blockIdx.y * cache_block_rows<DV>() + threadIdx.x / LPR;
-    char4 c[kCacheRows];
+    const int r0 = block * cache_block_rows<DV>() + threadIdx.x / LPR;
+    uint2 c[kCacheRows];
     float sc[kCacheRows];
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
         const int r = r0 + i * RPB;
-        const bool in = there && r < rows;
-        const size_t row = in ? (size_t)slot * rows + r : 0;
-        c[i] = make_char4(0, 0, 0, 0);
-        if (in) c[i] = reinterpret_cast<const char4*>(cache + row * DV)[lane];
-        sc[i] = in ? scale[row] : 0.f;
+        c[i] = make_uint2(0u, 0u);
+        sc[i] = 0.f;
+        if (there && r < rows) {
+            const size_t row = (size_t)slot * rows + r;
+            c[i] = reinterpret_cast<const uint2*>(cache + row * DV)[lane];
+            sc[i] = scale[row];
+        }
     }
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
         const int r = r0 + i * RPB;
-        if (r < rows)
-            __stcs(reinterpret_cast<float4*>(S + ((size_t)n * rows + r) * DV) + lane,
-                   make_float4((float)c[i].x * sc[i], (float)c[i].y * sc[i], (float)c[i].z * sc[i],
-                               (float)c[i].w * sc[i]));
+        if (r >= rows) break;
+        Float8 x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x.v[e] = (float)(int8_t)((e < 4 ? c[i].x : c[i].y) >> (8 * (e & 3))) * sc[i];
+        st_stream8(S + ((size_t)n * rows + r) * DV + 8 * lane, x);
     }
 }
 
@@ -117,11 +151,13 @@ inline cudaError_t launch_state_cache_write(const float* S, int8_t* cache, float
 {
     LaunchScope ls("state_cache_write", stream);
     const int per = dv == 128 ? cache_block_rows<128>() : cache_block_rows<64>();
-    const dim3 grid(N, (rows + per - 1) / per);
+    const int blocks = (rows + per - 1) / per;
+    if ((long long)N * blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)(N * blocks);
     if (dv == 128)
-        state_cache_write_kernel<128><<<grid, kCacheThreads, 0, stream>>>(S, cache, scale, slots, N, num_slots, rows);
+        state_cache_write_kernel<128><<<grid, kCacheThreads, 0, stream>>>(S, cache, scale, slots, N, num_slots, rows, blocks);
     else
-        state_cache_write_kernel<64><<<grid, kCacheThreads, 0, stream>>>(S, cache, scale, slots, N, num_slots, rows);
+        state_cache_write_kernel<64><<<grid, kCacheThreads, 0, stream>>>(S, cache, scale, slots, N, num_slots, rows, blocks);
     return cudaGetLastError();
 }
 
@@ -130,11 +166,13 @@ inline cudaError_t launch_state_cache_read(const int8_t* cache, const float* sca
 {
     LaunchScope ls("state_cache_read", stream);
     const int per = dv == 128 ? cache_block_rows<128>() : cache_block_rows<64>();
-    const dim3 grid(N, (rows + per - 1) / per);
+    const int blocks = (rows + per - 1) / per;
+    if ((long long)N * blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)(N * blocks);
     if (dv == 128)
-        state_cache_read_kernel<128><<<grid, kCacheThreads, 0, stream>>>(cache, scale, slots, S, num_slots, rows);
+        state_cache_read_kernel<128><<<grid, kCacheThreads, 0, stream>>>(cache, scale, slots, S, num_slots, rows, blocks);
     else
-        state_cache_read_kernel<64><<<grid, kCacheThreads, 0, stream>>>(cache, scale, slots, S, num_slots, rows);
+        state_cache_read_kernel<64><<<grid, kCacheThreads, 0, stream>>>(cache, scale, slots, S, num_slots, rows, blocks);
     return cudaGetLastError();
 }
 

@@ -7,7 +7,6 @@ and importing a missing or unbuilt library raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -555,20 +554,29 @@ def gated_rmsnorm(o: torch.Tensor, z: torch.Tensor, weight: Optional[torch.Tenso
     return out
 
 
-@contextlib.contextmanager
-def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
+class _on:
     """Device and stream of a call: outputs and workspaces allocated inside belong to the launch stream,
-    and the tensors' device is current for the launches.  Yields the stream handle."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    if stream is None and torch.cuda.current_device() == dev.index:
-        yield torch.cuda.current_stream(dev).cuda_stream
-    elif stream is None:
-        with torch.cuda.device(dev):
-            yield torch.cuda.current_stream(dev).cuda_stream
-    else:
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+    and the tensors' device is current for the launches.  Enters as the stream handle."""
+    __slots__ = ("dev", "stream", "ctx")
+
+    def __init__(self, dev: torch.device, stream: Optional[torch.cuda.Stream]):
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        self.dev, self.stream, self.ctx = dev, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.dev.index:
+            self.ctx = torch.cuda.device(self.dev)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        # the raw handle of the current stream, without a Stream object around it
+        return self.stream.cuda_stream if self.stream else torch._C._cuda_getCurrentRawStream(self.dev.index)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
 
 def _shape(t: torch.Tensor, name: str, want):
@@ -576,12 +584,19 @@ def _shape(t: torch.Tensor, name: str, want):
         raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
 
 
+def _fits(t: torch.Tensor, name: str, shape, dtype, dev):
+    """Raises unless ``t`` is a contiguous tensor of that shape, type and device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
+    _req(t, name, dtype, dev)
+    _shape(t, name, shape)
+
+
 def _given(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> torch.Tensor:
     """An output the caller gave, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    _req(t, name, dtype, dev)
-    _shape(t, name, shape)
+    _fits(t, name, shape, dtype, dev)
     return t
 
 
@@ -597,8 +612,7 @@ def _gdn_inputs(q, k, v, log_alpha, beta, cu_seqlens, states):
     for t, name, dt, shape in ((k, "k", q.dtype, q.shape), (v, "v", q.dtype, (B, T, H, dv)),
                                (log_alpha, "log_alpha", torch.float32, (B, T, H)),
                                (beta, "beta", torch.float32, (B, T, H))):
-        _req(t, name, dt, dev)
-        _shape(t, name, shape)
+        _fits(t, name, shape, dt, dev)
     if Hk == 0 or H % Hk != 0:
         raise ValueError(f"v's {H} heads must be a multiple of q's and k's {Hk}")
     N = B
@@ -609,8 +623,7 @@ def _gdn_inputs(q, k, v, log_alpha, beta, cu_seqlens, states):
         N = cu_seqlens.numel() - 1
     for t, name in states:
         if t is not None:
-            _req(t, name, torch.float32, dev)
-            _shape(t, name, (N, H, dk, dv))
+            _fits(t, name, (N, H, dk, dv), torch.float32, dev)
     return B, T, H, Hk, dk, dv, N
 
 
@@ -684,8 +697,7 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: 
     those keys."""
     B, T, H, Hk, dk, dv, N = _gdn_inputs(q, k, v, log_alpha, beta, cu_seqlens, ((S0, "S0"), (dS_final, "dS_final")))
     lib, dev, dt = load_library(), q.device, _dt(q)
-    _req(dout, "dout", q.dtype, dev)
-    _shape(dout, "dout", (B, T, H, dv))
+    _fits(dout, "dout", (B, T, H, dv), q.dtype, dev)
     want = {"dq": (q.shape, q.dtype), "dk": (q.shape, q.dtype), "dv": (v.shape, q.dtype),
             "dlog_alpha": ((B, T, H), torch.float32), "dbeta": ((B, T, H), torch.float32)}
     if want_dS0:
@@ -720,12 +732,11 @@ def gdn_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha
     for t, name, kind, shape in ((k, "k", q.dtype, q.shape), (v, "v", q.dtype, (N, H, dv)),
                                  (log_alpha, "log_alpha", torch.float32, (N, H)),
                                  (beta, "beta", torch.float32, (N, H)), (S, "S", torch.float32, (N, H, dk, dv))):
-        _req(t, name, kind, dev)
-        _shape(t, name, shape)
+        _fits(t, name, shape, kind, dev)
     if Hk == 0 or H % Hk != 0:
         raise ValueError(f"v's {H} heads must be a multiple of q's and k's {Hk}")
     with _on(dev, stream) as sh:
-        out = _given(out, "out", (N, H, dv), q.dtype, dev)
+        out = torch.empty_like(v) if out is None else _given(out, "out", (N, H, dv), q.dtype, dev)
         _check("kda_gdn_decode_step",
                load_library().kda_gdn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(S),
                                                   _ptr(out), N, H, Hk, dk, dv, dt, sh))
@@ -737,8 +748,7 @@ def _cache_args(cache, scale, slots):
     dev = cache.device
     if cache.dim() != 4:
         raise ValueError("cache must be [num_slots, H, dk, dv]")
-    _req(scale, "scale", torch.float32, dev)
-    _shape(scale, "scale", cache.shape[:3])
+    _fits(scale, "scale", cache.shape[:3], torch.float32, dev)
     _req(slots, "slots", torch.int32, dev)
     if slots.dim() != 1:
         raise ValueError("slots must be [N]")
@@ -753,8 +763,7 @@ def state_cache_write(S: torch.Tensor, cache: torch.Tensor, scale: torch.Tensor,
     states that name the same slot the last is kept; a slot past the cache is skipped and reported by
     ``check()``."""
     dev, N, num_slots, H, dk, dv = _cache_args(cache, scale, slots)
-    _req(S, "S", torch.float32, dev)
-    _shape(S, "S", (N, H, dk, dv))
+    _fits(S, "S", (N, H, dk, dv), torch.float32, dev)
     with _on(dev, stream) as sh:
         _check("kda_state_cache_write",
                load_library().kda_state_cache_write(_ptr(S), _ptr(cache), _ptr(scale), _ptr(slots), N, num_slots, H,

@@ -395,7 +395,7 @@ kda_status kda_gdn_decode_step(const void* q, const void* k, const void* v, cons
  * A negative slot is "none": write skips that state and read returns zeros for it.  A slot >= num_slots
  * does the same and records KDA_ERR_INVALID_ARG for kda_check().  Where `slots` names a slot twice, write
  * keeps the state that comes later; read may name one as often as it likes.  Other slots are untouched.
- * Supported: dk, dv in {64, 128}; N >= 0.  S and cache 16-byte aligned, scale and slots 4-byte.
+ * Supported: dk, dv in {64, 128}; N >= 0.  S 32-byte aligned, cache 16-byte, scale and slots 4-byte.
  */
 kda_status kda_state_cache_write(const float* S, int8_t* cache, float* scale, const int32_t* slots, int N,
                                  int num_slots, int H, int dk, int dv, kda_stream_t stream);
