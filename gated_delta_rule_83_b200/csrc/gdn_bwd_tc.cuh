@@ -10,8 +10,8 @@
 //     dbeta_i = dR_i.v_i - 2^g_i k_i.(dR S^T)_i + (E . k k^T) row sum
 //     dg_i = q_i.dq_i + k_i.ka_i - k_i.kb_i,  dg_C += sum_j w_j k_j.(U dS'^T)_j + 2^g_C <S, dS'>
 //     dlog_alpha_i = sum of dg_m over m >= i in the chunk
-// Four passes: per-chunk matrices (gdn_prep), the forward states again, the reverse chain for dS' and dR,
-// and one CTA a (chunk, head) for the gradients.  dg is taken from row products of terms that belong to
+// Three passes: per-chunk matrices (gdn_prep); side by side the forward states again and the reverse chain
+// for dS' and dR (in segments, with a pass for their ends before); one CTA a (chunk, head) for the gradients.  dg is taken from row products of terms that belong to
 // this chunk, never from a sum over the whole sequence, whose cancellation would cost the small gates
 // their digits.  Splits and accuracy as in the forward: 4..7e-6 for every fp32 gradient.
 #pragma once
@@ -46,16 +46,19 @@ constexpr uint32_t kRMisc = 2 * kRStage, kRSmem = kRMisc + 512 + 1024;
 
 // ENDS: no outputs, only a segment's start cotangent from a zero (the last segment's: the given) end one
 template <bool ENDS>
-__global__ void __launch_bounds__(kRThreads, 1)
-gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_do,
-                     const float* __restrict__ dS_final, float* __restrict__ dS0, __nv_bfloat16* __restrict__ dv_out,
-                     const WsHeader* __restrict__ hdr, const int* __restrict__ off, const int32_t* __restrict__ cu,
-                     int Tseq, int N, int H, int G, int dkw, int dvw, const uint8_t* __restrict__ slots,
-                     const uint8_t* __restrict__ bslots, uint8_t* __restrict__ images, Segments sg)
+__device__ __forceinline__ void reverse_body(const CUtensorMap* tm_k, const CUtensorMap* tm_do,
+                                             const float* __restrict__ dS_final, float* __restrict__ dS0,
+                                             __nv_bfloat16* __restrict__ dv_out, const ChainArgs& ca,
+                                             const uint8_t* __restrict__ bslots, uint8_t* __restrict__ images,
+                                             const Segments& sg, int block)
 {
+    const int* __restrict__ off = ca.off;
+    const int32_t* __restrict__ cu = ca.cu;
+    const int Tseq = ca.Tseq, N = ca.N, H = ca.H, G = ca.G, dkw = ca.dk, dvw = ca.dv;
+    const uint8_t* __restrict__ slots = ca.slots;
     extern __shared__ uint8_t smem_raw[];
-    if (cu && hdr->bad) return;
-    const int sidx = blockIdx.x / H, h = blockIdx.x - sidx * H;
+    if (cu && ca.hdr->bad) return;
+    const int sidx = block / H, h = block - sidx * H;
     int n, seg, nseg;
     if (!find_segment(sidx, off, cu, Tseq, N, sg, n, seg, nseg)) return;
     if (ENDS && seg == 0) return;  // nothing ends at the first segment's start
@@ -113,8 +116,8 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 const size_t u = (size_t)(jb + c) * H + h;
                 mbar_arrive_expect_tx(f, kRStage);
                 for (int a = 0; a < 2; ++a) {
-                    tma_load_3d(st + kRK + 8192 * a, &tm_k, 64 * a, h / G, t, f);
-                    tma_load_3d(st + kRDo + 8192 * a, &tm_do, 64 * a, h, t, f);
+                    tma_load_3d(st + kRK + 8192 * a, tm_k, 64 * a, h / G, t, f);
+                    tma_load_3d(st + kRDo + 8192 * a, tm_do, 64 * a, h, t, f);
                 }
                 bulk_g2s(st + kRGq, bslots + u * kBwdSlot + kBwdQ, 32768, f);
                 bulk_g2s(st + kRP, bslots + u * kBwdSlot + kBwdP, 32768, f);
@@ -332,6 +335,23 @@ gdn_bwd_chain_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     fence_before_sync();
     __syncthreads();
     if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// Both chains of the backward in one launch, since neither needs the other and each alone leaves SMs idle: blocks
+// 0 .. nr - 1 reverse, the next nr forward, and with ENDS the next nr the forward transitions.
+template <bool ENDS>
+__global__ void __launch_bounds__(kRThreads, 1)
+gdn_bwd_chains_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_do, const float* S0, const float* dS_final, float* dS0,
+                      __nv_bfloat16* dv_out, const __grid_constant__ ChainArgs ca, const uint8_t* bslots, uint8_t* images,
+                      const __grid_constant__ Segments fwd, const __grid_constant__ Segments rev, int nr)
+{
+    const int b = blockIdx.x;
+    if (b < nr)
+        reverse_body<ENDS>(&tm_k, &tm_do, dS_final, dS0, dv_out, ca, bslots, images, rev, b);
+    else
+        chain_body<ENDS ? kChainEnds : kChainStates>(&tm_k, &tm_k, &tm_v, S0, nullptr, nullptr, ca, images, fwd,
+                                                     b < 2 * nr ? b - nr : b - 2 * nr, b >= 2 * nr);
 }
 
 // ----------------------------------------------------------------------------------------------------
@@ -729,7 +749,7 @@ inline BwdLayout bwd_layout(int max_chunks, int N, long long Ttot, int H, int dk
     l.bslots = l.slots + (size_t)units * kSlot;
     l.images = l.bslots + (size_t)units * kBwdSlot;
     l.segs = l.images + (size_t)units * kImages;
-    l.seg_bytes = segments_bytes(max_chunks, N, H);
+    l.seg_bytes = segments_bytes(max_chunks, N, H, true);
     l.dq = l.segs + 3 * l.seg_bytes;
     const size_t acc = grouped ? (size_t)Ttot * H * dk * sizeof(float) : 0;
     l.dk = l.dq + acc;
@@ -745,14 +765,15 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
 {
     alignas(64) CUtensorMap tq{}, tk{}, tv{}, tdo{};
     const long long units = (long long)max_chunks * H;
-    if (units > 0x7fffffffLL || ((long long)max_chunks + N) * H > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (units > 0x7fffffffLL || 3 * ((long long)max_chunks + N) * H > 0x7fffffffLL) return cudaErrorInvalidValue;
     const bool grouped = Hk != H;
     const BwdLayout lay = bwd_layout(max_chunks, N, Ttot, H, dkw, grouped);
-    const int len = Ttot > 0 ? segment_length(max_chunks, N, H) : 0;
+    uint8_t *slots = ws + lay.slots, *bslots = ws + lay.bslots, *images = ws + lay.images;
+    const int len = Ttot > 0 ? segment_length(max_chunks, N, H, true) : 0;
     float* segs = (float*)(ws + lay.segs);
     const Segments fwd{len, segs, (float*)((uint8_t*)segs + lay.seg_bytes)};
     const Segments rev{len, (float*)((uint8_t*)segs + 2 * lay.seg_bytes), fwd.M};
-    uint8_t *slots = ws + lay.slots, *bslots = ws + lay.bslots, *images = ws + lay.images;
+    const ChainArgs ca{hdr, off, cu, Tseq, N, H, H / Hk, dkw, dvw, slots};
     float *dq_acc = grouped ? (float*)(ws + lay.dq) : nullptr, *dk_acc = grouped ? (float*)(ws + lay.dk) : nullptr;
     cudaError_t e = cudaSuccess;
     if (Ttot > 0) {
@@ -760,31 +781,27 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
             !make_map(&tdo, dout, H, dvw, Ttot))
             return cudaErrorInvalidValue;
         e = launch_prep<true>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, slots, bslots, stream);
-        if (e == cudaSuccess)
-            e = run_chain<kChainStates>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, dkw, dvw, max_chunks,
-                                        slots, images, fwd, stream);
         if (e != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(gdn_bwd_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRSmem);
+    constexpr uint32_t kSmem = kRSmem > Chain<kChainStates>::Smem ? kRSmem : Chain<kChainStates>::Smem;
+    e = cudaFuncSetAttribute(gdn_bwd_chains_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(gdn_bwd_chain_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRSmem);
+        e = cudaFuncSetAttribute(gdn_bwd_chains_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)(max_segments(max_chunks, N, len) * H);
+    const int nr = (int)(max_segments(max_chunks, N, len) * H);
     if (len) {
         {
             LaunchScope ls("gdn_bwd_ends", stream);
-            gdn_bwd_chain_kernel<true><<<grid, kRThreads, kRSmem, stream>>>(
-                tk, tdo, dS_final, nullptr, nullptr, hdr, off, cu, Tseq, N, H, H / Hk, dkw, dvw, slots, bslots,
-                nullptr, rev);
+            gdn_bwd_chains_kernel<true><<<3 * nr, kRThreads, kSmem, stream>>>(tk, tv, tdo, S0, dS_final, nullptr, nullptr, ca,
+                                                                            bslots, nullptr, fwd, rev, nr);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
-        if ((e = launch_join<true>(hdr, off, cu, Tseq, N, H, rev, stream)) != cudaSuccess) return e;
+        if ((e = launch_join(ca, fwd, &rev, stream)) != cudaSuccess) return e;
     }
     {
-        LaunchScope ls("gdn_bwd_chain", stream);
-        gdn_bwd_chain_kernel<false><<<grid, kRThreads, kRSmem, stream>>>(
-            tk, tdo, dS_final, dS0, (__nv_bfloat16*)dv, hdr, off, cu, Tseq, N, H, H / Hk, dkw, dvw, slots, bslots,
-            images, rev);
+        LaunchScope ls("gdn_bwd_chains", stream);
+        gdn_bwd_chains_kernel<false><<<2 * nr, kRThreads, kSmem, stream>>>(tk, tv, tdo, S0, dS_final, dS0, (__nv_bfloat16*)dv,
+                                                                         ca, bslots, images, fwd, rev, nr);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (Ttot == 0) return cudaSuccess;

@@ -21,6 +21,8 @@
 
 #include <cuda.h>
 
+#include <cmath>
+
 #include "common.cuh"
 #include "prefill_tc.cuh"
 #include "profile.cuh"
@@ -583,20 +585,31 @@ __device__ __forceinline__ void zero_tail_rows(uint8_t* atom, int L)
         *reinterpret_cast<uint4*>(atom + (L + (e >> 3)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
 
+// what the chains of a call share
+struct ChainArgs {
+    const WsHeader* hdr;
+    const int* off;
+    const int32_t* cu;
+    int Tseq, N, H, G, dk, dv;
+    const uint8_t* slots;
+};
+
+// chain `block` (segment * H + head); trans: kChainEnds from the identity, without v
 template <int MODE>
-__global__ void __launch_bounds__(Chain<MODE>::kThreads, 1)
-gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const float* S0, float* S_final,
-                 __nv_bfloat16* __restrict__ out, const WsHeader* __restrict__ hdr, const int* __restrict__ off,
-                 const int32_t* __restrict__ cu, int Tseq, int N, int H, int G, int dkw, int dvw,
-                 const uint8_t* __restrict__ slots, uint8_t* __restrict__ images, Segments sg)
+__device__ __forceinline__ void chain_body(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                           const float* S0, float* S_final, __nv_bfloat16* __restrict__ out,
+                                           const ChainArgs& ca, uint8_t* __restrict__ images, const Segments& sg, int block,
+                                           bool trans)
 {
+    const int* __restrict__ off = ca.off;
+    const int32_t* __restrict__ cu = ca.cu;
+    const int Tseq = ca.Tseq, N = ca.N, H = ca.H, G = ca.G, dkw = ca.dk, dvw = ca.dv;
+    const uint8_t* __restrict__ slots = ca.slots;
     using C = Chain<MODE>;
     constexpr bool kOut = MODE == kChainOut;
     extern __shared__ uint8_t smem_raw[];
-    if (cu && hdr->bad) return;
-    const int sidx = blockIdx.x / H, h = blockIdx.x - sidx * H;
-    const bool trans = MODE == kChainEnds && blockIdx.y == 1;  // from the identity, without v
+    if (cu && ca.hdr->bad) return;
+    const int sidx = block / H, h = block - sidx * H;
     int n, seg, nseg;
     if (!find_segment(sidx, off, cu, Tseq, N, sg, n, seg, nseg)) return;
     // nothing starts from the last segment's end, and the first one's start is known
@@ -659,9 +672,9 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const uint8_t* slot = slots + ((size_t)(jb + it) * H + h) * kSlot;
                 mbar_arrive_expect_tx(f, kOut ? 49152 + kSlot : 32768 + 16384 + 1024);
                 for (int a = 0; a < 2; ++a) {
-                    tma_load_3d(st + C::K + 8192 * a, &tm_k, 64 * a, h / G, t, f);
-                    if (kOut) tma_load_3d(st + C::Q + 8192 * a, &tm_q, 64 * a, h / G, t, f);
-                    tma_load_3d(st + C::V + 8192 * a, &tm_v, 64 * a, h, t, f);
+                    tma_load_3d(st + C::K + 8192 * a, tm_k, 64 * a, h / G, t, f);
+                    if (kOut) tma_load_3d(st + C::Q + 8192 * a, tm_q, 64 * a, h / G, t, f);
+                    tma_load_3d(st + C::V + 8192 * a, tm_v, 64 * a, h, t, f);
                 }
                 if (kOut) {
                     bulk_g2s(st + C::Slot, slot, kSlot, f);
@@ -955,6 +968,15 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
+template <int MODE>
+__global__ void __launch_bounds__(Chain<MODE>::kThreads, 1)
+gdn_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const float* S0, float* S_final, __nv_bfloat16* out,
+                 const __grid_constant__ ChainArgs ca, const __grid_constant__ Segments sg)
+{
+    chain_body<MODE>(&tm_q, &tm_k, &tm_v, S0, S_final, out, ca, nullptr, sg, blockIdx.x, blockIdx.y == 1);
+}
+
 // [tokens][heads][d] bf16 as a 3-D map of 64-token, 64-channel boxes that land 128B-swizzled
 inline bool make_map(CUtensorMap* m, const void* base, int heads, int d, long long ntok)
 {
@@ -988,16 +1010,17 @@ cudaError_t launch_prep(const CUtensorMap& tq, const CUtensorMap& tk, const floa
 constexpr int kJoinCols = 16, kJoinThreads = 256;
 constexpr uint32_t kJoinSmem = 65536 + 1024;
 template <bool REVERSE>
-__global__ void __launch_bounds__(kJoinThreads)
-gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, const int32_t* __restrict__ cu, int Tseq,
-                int H, Segments sg)
+__device__ __forceinline__ void join_body(const ChainArgs& ca, const Segments& sg, int slice)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_first;
     __shared__ __align__(8) uint64_t s_bar;
-    if (cu && hdr->bad) return;
+    const int* __restrict__ off = ca.off;
+    const int32_t* __restrict__ cu = ca.cu;
+    const int Tseq = ca.Tseq, H = ca.H;
+    if (cu && ca.hdr->bad) return;
     const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int v = blockIdx.z * kJoinCols + (lane & 15), k0 = 64 * (lane >> 4);
+    const int v = slice * kJoinCols + (lane & 15), k0 = 64 * (lane >> 4);
     uint8_t* sm = align1024(smem_raw);
     const float* sM = reinterpret_cast<const float*>(sm);
     const uint32_t bar = smem_u32(&s_bar);
@@ -1059,83 +1082,70 @@ gdn_join_kernel(const WsHeader* __restrict__ hdr, const int* __restrict__ off, c
     }
 }
 
-// Chunks a segment, from the number of chains and their length (for packed sequences the mean; the lengths
-// are on the device).  Modelled in microseconds: a chunk costs 3.1 in the real pass and 2.25 in the ends',
-// the join 4 a segment; past one CTA an SM a pass grows with the CTAs, and by 0.7 for its last, part-filled wave.
-// Measured at 512 chunks x 32 heads: 3 segments 385 + 519 us, 4 segments 510 + 437, none 1520.
-inline int segment_length(int max_chunks, int N, int H)
+// slices 0 .. 7 forward, 8 .. 15 (the backward only) reverse
+__global__ void __launch_bounds__(kJoinThreads)
+gdn_join_kernel(const __grid_constant__ ChainArgs ca, const __grid_constant__ Segments fwd,
+                const __grid_constant__ Segments rev)
 {
-    constexpr int kSms = 148, kMaxSeqs = 1024, kMinLen = 4;
+    constexpr int kSlices = 128 / kJoinCols;
+    if (blockIdx.z < kSlices) join_body<false>(ca, fwd, blockIdx.z);
+    else join_body<true>(ca, rev, blockIdx.z - kSlices);
+}
+
+// Chunks a segment, from the number of chains c and their length L (for packed sequences the mean; the lengths
+// are on the device).  G segments put c G CTAs into the real pass and c (2 G - 3) into the ends' (backward, both
+// chains side by side: 2 c G and c (3 G - 4)); CTAs run one an SM, so G stays where neither needs a second
+// wave.  Within that, a segment costs about 7 us (join, start of two passes), which against 5.2 (6.3) us a chunk
+// of the two passes is least at G = sqrt(0.75 L).  Without segments a chunk costs 3.0 (3.9) us.
+// Measured at best and without segments, us: prefill, 512 chunks, 32 heads G = 3 1219, 1788; 16 heads 6 674, 1772;
+// 2 heads 16 289, 1473; 80 chains of 256 chunks 1 1159 (2: 1463); backward, 32 heads 2 3248, 3531; 8 heads 8 986,
+// 2401; 32 chains of 16 chunks 1 142 (2: 154).
+inline int segment_length(int max_chunks, int N, int H, bool bwd)
+{
+    constexpr double kSms = 148;
+    constexpr int kMaxSeqs = 1024;
     if (N > kMaxSeqs || max_chunks == 0) return 0;
-    const long long chains = (long long)N * H;
+    const double c = (double)N * H;
     const int L = (max_chunks + N - 1) / N;
-    auto waves = [&](long long ctas) { return ctas <= kSms ? 1.0 : (double)ctas / kSms + 0.7; };
-    double best = waves(chains) * L * 3.1;
-    int len = 0;
-    for (int g = 2; g <= 64 && L / g >= kMinLen; ++g) {
-        const int l = (L + g - 1) / g;
-        const double t = (waves(chains * g) * 3.1 + waves(chains * (2 * g - 3)) * 2.25) * l + 4.0 * (g - 2) + 10.0;
-        if (t < 0.95 * best) {
-            best = t;
-            len = l;
-        }
-    }
-    return len;
+    const double fit = bwd ? fmin(kSms / (2 * c), (kSms / c + 4) / 3) : fmin(kSms / c, (kSms / c + 3) / 2);
+    const int G = (int)fmin(fit, sqrt(0.75 * L));
+    if (G < 2 || (bwd ? 6.3 : 5.2) * L / G + 7.0 * G + 10.0 > 0.95 * (bwd ? 3.9 : 3.0) * L) return 0;
+    return (L + G - 1) / G;
 }
 inline long long max_segments(int max_chunks, int N, int len) { return len ? max_chunks / len + N : N; }
-inline size_t segments_bytes(int max_chunks, int N, int H)
+inline size_t segments_bytes(int max_chunks, int N, int H, bool bwd)
 {
-    const int len = segment_length(max_chunks, N, H);
+    const int len = segment_length(max_chunks, N, H, bwd);
     return len ? (size_t)max_segments(max_chunks, N, len) * H * 65536 : 0;
 }
 
 template <int MODE>
 cudaError_t launch_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const float* S0,
-                         float* S_final, void* out, const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq,
-                         int N, int H, int Hk, int dk, int dv, int max_chunks, const uint8_t* slots, uint8_t* images,
-                         const Segments& sg, cudaStream_t stream)
+                         float* S_final, void* out, const ChainArgs& ca, int max_chunks, const Segments& sg,
+                         cudaStream_t stream)
 {
     using C = Chain<MODE>;
     const cudaError_t e = cudaFuncSetAttribute(gdn_chain_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
     if (e != cudaSuccess) return e;
-    LaunchScope ls(MODE == kChainOut ? "gdn_chain" : MODE == kChainStates ? "gdn_bwd_states" : "gdn_ends", stream);
-    const dim3 grid((unsigned)(max_segments(max_chunks, N, sg.len) * H), MODE == kChainEnds ? 2 : 1);
-    gdn_chain_kernel<MODE><<<grid, C::kThreads, C::Smem, stream>>>(tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, hdr, off,
-                                                                  cu, Tseq, N, H, H / Hk, dk, dv, slots, images, sg);
+    LaunchScope ls(MODE == kChainOut ? "gdn_chain" : "gdn_ends", stream);
+    const dim3 grid((unsigned)(max_segments(max_chunks, ca.N, sg.len) * ca.H), MODE == kChainEnds ? 2 : 1);
+    gdn_chain_kernel<MODE><<<grid, C::kThreads, C::Smem, stream>>>(tq, tk, tv, S0, S_final, (__nv_bfloat16*)out, ca, sg);
     return cudaGetLastError();
 }
-template <bool REVERSE>
-cudaError_t launch_join(const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq, int N, int H, const Segments& sg,
-                        cudaStream_t stream)
+inline cudaError_t launch_join(const ChainArgs& ca, const Segments& fwd, const Segments* rev, cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(gdn_join_kernel<REVERSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmem);
+    const cudaError_t e = cudaFuncSetAttribute(gdn_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinSmem);
     if (e != cudaSuccess) return e;
     LaunchScope ls("gdn_join", stream);
-    gdn_join_kernel<REVERSE><<<dim3(N, H, 128 / kJoinCols), kJoinThreads, kJoinSmem, stream>>>(hdr, off, cu, Tseq, H, sg);
+    gdn_join_kernel<<<dim3(ca.N, ca.H, 128 / kJoinCols * (rev ? 2 : 1)), kJoinThreads, kJoinSmem, stream>>>(
+        ca, fwd, rev ? *rev : fwd);
     return cudaGetLastError();
 }
 
-// the chain of all sequences, segmented where that pays; seg_ws: twice segments_bytes()
-template <int MODE>
-cudaError_t run_chain(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const float* S0,
-                      float* S_final, void* out, const WsHeader* hdr, const int* off, const int32_t* cu, int Tseq, int N,
-                      int H, int Hk, int dk, int dv, int max_chunks, const uint8_t* slots, uint8_t* images, Segments sg,
-                      cudaStream_t stream)
-{
-    if (sg.len) {
-        cudaError_t e = launch_chain<kChainEnds>(tq, tk, tv, S0, nullptr, nullptr, hdr, off, cu, Tseq, N, H, Hk, dk, dv,
-                                                 max_chunks, slots, nullptr, sg, stream);
-        if (e == cudaSuccess) e = launch_join<false>(hdr, off, cu, Tseq, N, H, sg, stream);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_chain<MODE>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, dk, dv, max_chunks, slots, images,
-                              sg, stream);
-}
-
-// bytes behind the header and the chunk table
+// bytes behind the header and the chunk table: slots, segment states (end, transition)
 inline size_t fwd_bytes(int max_chunks, int N, int H)
 {
-    return (size_t)max_chunks * H * kSlot + 2 * segments_bytes(max_chunks, N, H);
+    return (size_t)max_chunks * H * kSlot + 2 * segments_bytes(max_chunks, N, H, false);
 }
 
 inline cudaError_t launch_fwd(const void* q, const void* k, const void* v, const float* la, const float* beta,
@@ -1147,16 +1157,21 @@ inline cudaError_t launch_fwd(const void* q, const void* k, const void* v, const
     const long long units = (long long)max_chunks * H;
     if (units > 0x7fffffffLL || ((long long)max_chunks + N) * H > 0x7fffffffLL) return cudaErrorInvalidValue;
     uint8_t* segs = ws + units * kSlot;
-    const size_t sb = segments_bytes(max_chunks, N, H);
-    const Segments sg{Ttot > 0 ? segment_length(max_chunks, N, H) : 0, (float*)segs, (float*)(segs + sb)};
+    const size_t sb = segments_bytes(max_chunks, N, H, false);
+    const Segments sg{Ttot > 0 ? segment_length(max_chunks, N, H, false) : 0, (float*)segs, (float*)(segs + sb)};
+    const ChainArgs ca{hdr, off, cu, Tseq, N, H, H / Hk, dk, dv, ws};
+    cudaError_t e = cudaSuccess;
     if (Ttot > 0) {
         if (!make_map(&tq, q, Hk, dk, Ttot) || !make_map(&tk, k, Hk, dk, Ttot) || !make_map(&tv, v, H, dv, Ttot))
             return cudaErrorInvalidValue;
-        const cudaError_t e = launch_prep<false>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, ws, nullptr, stream);
-        if (e != cudaSuccess) return e;
+        e = launch_prep<false>(tq, tk, la, beta, hdr, off, cu, Tseq, N, H, Hk, units, ws, nullptr, stream);
     }
-    return run_chain<kChainOut>(tq, tk, tv, S0, S_final, out, hdr, off, cu, Tseq, N, H, Hk, dk, dv, max_chunks, ws, nullptr,
-                                sg, stream);
+    if (e == cudaSuccess && sg.len) {
+        e = launch_chain<kChainEnds>(tq, tk, tv, S0, nullptr, nullptr, ca, max_chunks, sg, stream);
+        if (e == cudaSuccess) e = launch_join(ca, sg, nullptr, stream);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_chain<kChainOut>(tq, tk, tv, S0, S_final, out, ca, max_chunks, sg, stream);
 }
 
 }  // namespace gdn
