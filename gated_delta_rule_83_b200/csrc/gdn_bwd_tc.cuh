@@ -72,7 +72,7 @@ __device__ __forceinline__ void reverse_body(const CUtensorMap* tm_k, const CUte
                                : StateRef{ENDS ? nullptr : sg.F + part + (size_t)H * 16384, 128, 128, 128};
     const StateRef end = ENDS ? StateRef{sg.F + part, 128, 128, 128}
                               : StateRef{dS0 && seg == 0 ? dS0 + mine : nullptr, dvw, dkw, dvw};
-    uint8_t* sm = align1024(smem_raw);
+    uint8_t* sm = aligned_smem(smem_raw);
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + kRMisc;
     const uint32_t bar_full = bars, bar_empty = bars + 16, bar_k = bars + 32, bar_d = bars + 48, bar_s = bars + 64,
@@ -389,7 +389,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     int h, n, L;
     long long t0;
     tc_unit(blockIdx.x, H, off, cu, Tseq, N, h, n, t0, L);
-    uint8_t* sm = align1024(smem_raw);
+    uint8_t* sm = aligned_smem(smem_raw);
     const uint32_t sb = smem_u32(sm);
     float* s_g = reinterpret_cast<float*>(sm + kGMisc);   // [64]
     float* s_b = s_g + 64;                                // [64]

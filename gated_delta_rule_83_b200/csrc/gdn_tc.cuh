@@ -43,6 +43,9 @@ __device__ __forceinline__ bool elect_one()
     asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
     return p != 0;
 }
+// the dynamic shared memory from its first 1024-byte boundary on, still known to be shared memory: through a
+// pointer cast from an integer every access would be a generic one
+__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* raw) { return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u); }
 template <typename T> __device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // D[tmem] (+)= A[tmem] * B[smem desc]: A row i in lane i, two consecutive K elements a 32-bit column
@@ -280,7 +283,7 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     int h, n, L;
     long long t0;
     tc_unit(blockIdx.x, H, off, cu, Tseq, N, h, n, t0, L);
-    uint8_t* sm = align1024(smem_raw);
+    uint8_t* sm = aligned_smem(smem_raw);
     const uint32_t sb = smem_u32(sm);
     float* sA = reinterpret_cast<float*>(sm + kPrepA);
     float* sY = reinterpret_cast<float*>(sm + kPrepY);
@@ -623,7 +626,7 @@ __device__ __forceinline__ void chain_body(const CUtensorMap* tm_q, const CUtens
                                     : StateRef{MODE == kChainEnds ? nullptr : sg.F + part - (size_t)H * 16384, 128, 128, 128};
     const StateRef end = MODE == kChainEnds ? StateRef{(trans ? sg.M : sg.F) + part, 128, 128, 128}
                                             : StateRef{S_final && seg == nseg - 1 ? S_final + mine : nullptr, dvw, dkw, dvw};
-    uint8_t* sm = align1024(smem_raw);
+    uint8_t* sm = aligned_smem(smem_raw);
     const uint32_t sb = smem_u32(sm);
     const uint32_t bars = sb + C::Misc;
     const uint32_t bar_full = bars, bar_empty = bars + 16, bar_k = bars + 32, bar_u = bars + 48, bar_d = bars + 64,
@@ -1021,7 +1024,7 @@ __device__ __forceinline__ void join_body(const ChainArgs& ca, const Segments& s
     if (cu && ca.hdr->bad) return;
     const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int v = slice * kJoinCols + (lane & 15), k0 = 64 * (lane >> 4);
-    uint8_t* sm = align1024(smem_raw);
+    uint8_t* sm = aligned_smem(smem_raw);
     const float* sM = reinterpret_cast<const float*>(sm);
     const uint32_t bar = smem_u32(&s_bar);
     // the sequence's first segment: the segments of those before it
