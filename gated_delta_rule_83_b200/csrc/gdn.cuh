@@ -15,7 +15,8 @@ gdn_spread_gate_kernel(const float* __restrict__ la, float4* __restrict__ out, l
 {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // a float4 of one (token, head)
     if (i >= n) return;
-    const float a = la[i / quads];
+    float a = la[i / quads];
+    a = a < -104.f ? -104.f : a;  // e^-104 rounds every state to zero, and -inf would make differences NaN
     out[i] = make_float4(a, a, a, a);
 }
 

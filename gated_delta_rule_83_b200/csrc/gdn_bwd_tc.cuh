@@ -393,7 +393,8 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t sb = smem_u32(sm);
     float* s_g = reinterpret_cast<float*>(sm + kGMisc);   // [64]
     float* s_b = s_g + 64;                                // [64]
-    float* s_red = s_g + 128;                             // [4 sums][4 parts][64 rows]
+    float* s_gl = s_g + 128;                              // [64]
+    float* s_red = s_g + 192;                             // [4 sums][4 parts][64 rows]
     float* s_sds = s_red + 1024;                          // [8]
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + kGMisc + 6144);
     const uint32_t bar_in = sb + kGMisc + 6160, bar_s = bar_in + 8, bar_ds = bar_in + 16, bar_read = bar_in + 24,
@@ -419,7 +420,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         bulk_g2s(sb + kGU, img + kImgU, 65536, bar_in);  // U and dR
         bulk_g2s(sb + kGS, img + kImgS, 65536, bar_s);
     }
-    if (warp == 1) load_scalars(la, beta, t0, L, H, h, s_g, s_b);
+    if (warp == 1) load_scalars(la, beta, t0, L, H, h, s_g, s_gl, s_b);
     if (warp == 2) {
         tmem_alloc(smem_u32(s_tmem), 512);
         tmem_relinquish();
@@ -487,7 +488,8 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t tl = tmem + ((uint32_t)(32 * wq) << 16);
     const int c0 = 64 * (lane >> 4) + 32 * hw;   // this thread's channels
     const int j0 = 32 * (lane >> 4) + 16 * hw;   // its columns of the 64 x 64 products
-    const float gi = s_g[r], bi = s_b[r], gam = ex2_approx(gi), wi = ex2_approx(s_g[63] - gi);
+    const float gi = s_g[r], gli = s_gl[r], bi = s_b[r], gam = ex2_approx(gi),
+                wi = ex2_approx((s_g[63] - gi) + (s_gl[63] - gli));
     uint4 sh[8], sl[8];  // this thread's share of S for <S, dS'>, before dS' takes its place
     ok = ok && mbar_wait(bar_s, 0);
 #pragma unroll
@@ -511,7 +513,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
         for (int m = 0; m < 16; ++m) {
             const int j = j0 + m;
-            const float D = ex2_approx(gi - s_g[j]);
+            const float D = ex2_approx((gi - s_g[j]) + (gli - s_gl[j]));
             x[m] = (j <= r && r < L) ? x[m] * D : 0.f;
             const float e = (j < r && r < L) ? -y[m] * D : 0.f;
             db = fmaf(e, z[m], db);

@@ -234,9 +234,12 @@ __device__ __forceinline__ void invert_unit_lower(float* __restrict__ sA, float*
 }
 
 // g (log2 units, cumulative) and beta of a chunk's 64 tokens into shared memory, by one warp; tokens past
-// the chunk's end carry no gate and no weight
+// the chunk's end carry no gate and no weight.  g is summed in 64 bits and kept as hi + lo: behind a token that
+// forgets all (log alpha = -100, say) the decays between later tokens are differences of two large g, which
+// in 32 bits alone would be off by 1e-5.  A gate below 2^-150 is 2^-150, which rounds every state to zero, so that
+// log alpha = -inf needs no care elsewhere.
 __device__ __forceinline__ void load_scalars(const float* __restrict__ la, const float* __restrict__ beta, long long t0,
-                                             int L, int H, int h, float* s_g, float* s_b)
+                                             int L, int H, int h, float* s_g, float* s_gl, float* s_b)
 {
     const int l = threadIdx.x & 31;
     float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
@@ -248,15 +251,19 @@ __device__ __forceinline__ void load_scalars(const float* __restrict__ la, const
         a1 = la[(size_t)(t0 + 2 * l + 1) * H + h] * kLog2e;
         b1 = beta[(size_t)(t0 + 2 * l + 1) * H + h];
     }
-    float s = a0 + a1;
+    a0 = a0 < -150.f ? -150.f : a0;  // (a NaN stays one)
+    a1 = a1 < -150.f ? -150.f : a1;
+    double s = (double)a0 + (double)a1;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, s, d);
+        const double y = __shfl_up_sync(0xffffffffu, s, d);
         if (l >= d) s += y;
     }
-    float before = __shfl_up_sync(0xffffffffu, s, 1);
-    if (l == 0) before = 0.f;
-    *reinterpret_cast<float2*>(s_g + 2 * l) = make_float2(before + a0, s);
+    double first = __shfl_up_sync(0xffffffffu, s, 1);
+    first = (l == 0 ? 0.0 : first) + (double)a0;
+    const float h0 = (float)first, h1 = (float)s;
+    *reinterpret_cast<float2*>(s_g + 2 * l) = make_float2(h0, h1);
+    *reinterpret_cast<float2*>(s_gl + 2 * l) = make_float2((float)(first - (double)h0), (float)(s - (double)h1));
     *reinterpret_cast<float2*>(s_b + 2 * l) = make_float2(b0, b1);
 }
 
@@ -289,8 +296,9 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     float* sY = reinterpret_cast<float*>(sm + kPrepY);
     float* s_g = reinterpret_cast<float*>(sm + kPrepMisc);
     float* s_b = s_g + 64;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + kPrepMisc + 512);
-    const uint32_t bar_in = sb + kPrepMisc + 528, bar_mma = bar_in + 8;
+    float* s_gl = s_g + 128;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + kPrepMisc + 768);
+    const uint32_t bar_in = sb + kPrepMisc + 784, bar_mma = bar_in + 8;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -303,7 +311,7 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             tma_load_3d(sb + a * 16384 + 8192, &tm_q, 64 * a, h / G, (int)t0, bar_in);
         }
     }
-    if (warp == 1) load_scalars(la, beta, t0, L, H, h, s_g, s_b);
+    if (warp == 1) load_scalars(la, beta, t0, L, H, h, s_g, s_gl, s_b);
     if (warp == 2) {
         tmem_alloc(smem_u32(s_tmem), 64);
         tmem_relinquish();
@@ -350,7 +358,7 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     {
         float x[32];
         tmem_ld32(tmem + ((uint32_t)(32 * wq) << 16) + col0, x);
-        const float gi = s_g[i], bi = s_b[i];
+        const float gi = s_g[i], gli = s_gl[i], bi = s_b[i];
         const bool row = i < L, isA = wq < 2, above = col0 > 32 * (wq & 1);  // above the diagonal: zero
 #pragma unroll
         for (int m = 0; m < 32; m += 4) {
@@ -359,12 +367,13 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 continue;
             }
             const float4 g4 = *reinterpret_cast<const float4*>(s_g + col0 + m);
-            const float gj[4] = {g4.x, g4.y, g4.z, g4.w};
+            const float4 l4 = *reinterpret_cast<const float4*>(s_gl + col0 + m);
+            const float gj[4] = {g4.x, g4.y, g4.z, g4.w}, lj[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int j = col0 + m + e;
                 // the select comes last: what lies past the chunk's end may be anything
-                const float y = x[m + e] * ex2_approx(gi - gj[e]);
+                const float y = x[m + e] * ex2_approx((gi - gj[e]) + (gli - lj[e]));
                 x[m + e] = (row && (isA ? j < i : j <= i)) ? y : 0.f;
             }
         }
@@ -403,7 +412,7 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         float* sc = reinterpret_cast<float*>(img + kScal);
         const float gam = ex2_approx(s_g[tid]);
         sc[kGam + tid] = gam;
-        sc[kW + tid] = ex2_approx(s_g[63] - s_g[tid]);
+        sc[kW + tid] = ex2_approx((s_g[63] - s_g[tid]) + (s_gl[63] - s_gl[tid]));
         sc[kBeta + tid] = s_b[tid];
         sc[kNgam + tid] = -gam;
     }
@@ -615,14 +624,22 @@ __device__ __forceinline__ void chain_body(const CUtensorMap* tm_q, const CUtens
     const int sidx = block / H, h = block - sidx * H;
     int n, seg, nseg;
     if (!find_segment(sidx, off, cu, Tseq, N, sg, n, seg, nseg)) return;
-    // nothing starts from the last segment's end, and the first one's start is known
-    if (MODE == kChainEnds && (seg == nseg - 1 || (trans && seg == 0))) return;
+    const size_t mine = ((size_t)n * H + h) * dkw * dvw, part = ((size_t)sidx * H + h) * 16384;
+    if (MODE == kChainEnds && (seg == nseg - 1 || (trans && seg == 0))) {
+        // Nothing starts from the last segment's end, and the first one's start is known.  The last one's place
+        // keeps S0 instead: S_final may be S0, and the CTA that writes it is not the one that starts from it.
+        if (!trans && S0)
+            for (int e = threadIdx.x; e < dkw * dvw; e += Chain<MODE>::kThreads) sg.F[part + e] = S0[mine + e];
+        return;
+    }
     const int jb = chunks_before(off, cu, Tseq, n) + seg * sg.len, left = chunks_before(off, cu, Tseq, n + 1) - jb, nch = seg == nseg - 1 ? left : sg.len;
     long long s0, s1;
     seq_bounds(n, cu, Tseq, s0, s1);
     s0 += 64LL * seg * sg.len;
-    const size_t mine = ((size_t)n * H + h) * dkw * dvw, part = ((size_t)sidx * H + h) * 16384;
-    const StateRef start = seg == 0 ? StateRef{S0 ? const_cast<float*>(S0) + mine : nullptr, dvw, dkw, dvw}
+    float* s0p = !S0 ? nullptr
+                 : MODE == kChainEnds || nseg == 1 ? const_cast<float*>(S0) + mine
+                                                   : sg.F + ((size_t)(sidx + nseg - 1) * H + h) * 16384;
+    const StateRef start = seg == 0 ? StateRef{s0p, dvw, dkw, dvw}
                                     : StateRef{MODE == kChainEnds ? nullptr : sg.F + part - (size_t)H * 16384, 128, 128, 128};
     const StateRef end = MODE == kChainEnds ? StateRef{(trans ? sg.M : sg.F) + part, 128, 128, 128}
                                             : StateRef{S_final && seg == nseg - 1 ? S_final + mine : nullptr, dvw, dkw, dvw};

@@ -342,7 +342,7 @@ kda_status kda_chunk_fwd_gated(const void* q, const void* k, const void* v, cons
  *
  *   q, k       [B, T, Hk, dk] dt;  v [B, T, H, dv] dt: value head h reads q/k head h / (H / Hk).  H must
  *              be a multiple of Hk.
- *   log_alpha, beta  [B, T, H] fp32 (4-byte aligned; log_alpha <= 0 expected).
+ *   log_alpha, beta  [B, T, H] fp32 (4-byte aligned; log_alpha <= 0 expected, -inf = forget all).
  *   S0, cu_seqlens, num_seqs, out, S_final: as kda_chunk_fwd (S_final may alias S0).
  * Accuracy: sums and states are fp32, and every fp32 operand of a tensor-core product is split into two
  * bf16 parts (about 16 significant bits), so S_final is good to about 1e-5 for bf16 inputs as well.

@@ -264,6 +264,60 @@ def test_gate_extremes(dt, d_):
         check(g[x], ref[x], dt, x)
 
 
+@pytest.mark.parametrize("dt,d_", [(torch.bfloat16, 128), (torch.float32, 64)])
+@pytest.mark.parametrize("gate", [-30.0, -100.0, float("-inf")])
+def test_tokens_that_forget_all(dt, d_, gate):
+    """A gate that is zero or nearly so inside a chunk, at its border and twice in one: what lies before has no
+    weight, and the decays between the tokens behind keep their digits."""
+    d = make(13, dt, 2, 2, d_, d_, T=300, gate=4.0)
+    for t in (0, 5, 64, 70, 71, 191, 299):
+        d["log_alpha"][:, t, 0] = gate
+    out, S = run_fwd(d)
+    o_ref, s_ref = ref_fwd(d)
+    check(out, o_ref, dt, "out")
+    check(S, s_ref, dt, "S")
+    g, ref = run_bwd(d), ref_bwd(d)
+    for x in ("dq", "dk", "dv", "dlog_alpha", "dbeta", "dS0"):
+        check(g[x], ref[x], dt, x)
+
+
+def test_sequences_do_not_see_their_neighbours():
+    """Packed input in which one sequence holds NaN and infinities throughout, cotangents too: the others get
+    the very numbers they get without it."""
+    lens = [70, 100, 1, 63, 200]
+    d = make(14, torch.bfloat16, 2, 1, 128, 128, lens=lens)
+    a = (run_fwd(d), run_bwd(d))
+    lo, hi = 70, 170
+    for x, bad in (("q", float("nan")), ("k", float("inf")), ("v", float("nan")), ("dout", float("inf")),
+                   ("log_alpha", float("nan")), ("beta", float("nan"))):
+        d[x][:, lo:hi] = bad
+    d["S0"][1] = float("nan")
+    d["dS_final"][1] = float("inf")
+    b = (run_fwd(d), run_bwd(d))
+    rows = torch.cat([torch.arange(lo), torch.arange(hi, sum(lens))]).to(DEV)
+    seqs = torch.tensor([0, 2, 3, 4], device=DEV)
+    assert torch.equal(a[0][0][:, rows], b[0][0][:, rows]) and torch.equal(a[0][1][seqs], b[0][1][seqs])
+    for x in ("dq", "dk", "dv", "dlog_alpha", "dbeta"):
+        assert torch.equal(a[1][x][:, rows], b[1][x][:, rows]), x
+    assert torch.equal(a[1]["dS0"][seqs], b[1]["dS0"][seqs])
+
+
+@pytest.mark.parametrize("kw", [dict(T=4000, B=1), dict(lens=[3000, 10, 0, 1500])])
+def test_long_sequences_in_place(kw):
+    """Sequences long enough to be cut into segments, the state passed in place: as with a state of its own."""
+    d = make(15, torch.bfloat16, 1, 1, 128, 128, **kw)
+    out, S = run_fwd(d)
+    mine = d["S0"].clone()
+    m = kda()
+    out2, S2 = m.gdn_chunk_fwd(d["q"], d["k"], d["v"], d["log_alpha"], d["beta"], S0=mine, S_final=mine,
+                               cu_seqlens=d["cu"])
+    m.check()
+    assert S2 is mine and torch.equal(out, out2) and torch.equal(S, mine)
+    o_ref, s_ref = ref_fwd(d)
+    check(out, o_ref, torch.bfloat16, "out")
+    check(S, s_ref, torch.bfloat16, "S")
+
+
 def test_calls_repeat_bit_for_bit_and_leave_inputs():
     d = make(10, torch.bfloat16, 4, 2, 128, 128, lens=[100, 300, 7])
     before = {x: y.clone() for x, y in d.items() if y is not None}
