@@ -107,6 +107,7 @@ __device__ __forceinline__ void reverse_body(const CUtensorMap* tm_k, const CUte
     bool ok = true;
 
     if (warp == 9) {  // loads, two stages
+        int issued = 0;
         for (int it = 0; it < nch && ok; ++it) {
             const int s = it & 1, c = nch - 1 - it;
             if (it >= 2) ok = warp_wait(bar_empty + 8 * s, (uint32_t)((it >> 1) - 1) & 1u, s_abort);
@@ -124,9 +125,10 @@ __device__ __forceinline__ void reverse_body(const CUtensorMap* tm_k, const CUte
                 bulk_g2s(st + kRScal, slots + u * kSlot + kScal, 1024, f);
             }
             __syncwarp();
+            issued = ok ? it + 1 : issued;
         }
-        for (int it = nch > 2 ? nch - 2 : 0; it < nch; ++it)  // no copy outlives the CTA, whatever gave up
-            if (!ok) (void)mbar_wait(bar_full + 8 * (it & 1), (uint32_t)(it >> 1) & 1u);
+        for (int it = issued > 2 ? issued - 2 : 0; it < issued; ++it)  // no copy outlives the CTA, whatever gave up
+            (void)mbar_wait(bar_full + 8 * (it & 1), (uint32_t)(it >> 1) & 1u);
     } else if (warp == 8) {
         const uint32_t id64 = idesc_bf16(128, 64, false, false), id32 = idesc_bf16(128, 32, false, false),
                        id64m = idesc_bf16(128, 64, false, true), idE = idesc_bf16(128, 64, true, true),
@@ -684,6 +686,11 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     if (lane == 0) s_sds[warp] = sds;
     fence_before_sync();
     ok = __syncthreads_and(ok);
+    if (!ok && warp == 0) {  // no copy outlives the CTA
+        (void)mbar_wait(bar_in, 0);
+        (void)mbar_wait(bar_s, 0);
+        (void)mbar_wait(bar_ds, 0);
+    }
     if (warp == 2) tmem_dealloc(tmem, 512);
     if (warp == 0 && ok) {
         auto sum4 = [&](int k, int i) {

@@ -336,6 +336,7 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         __syncwarp();
     }
     ok = __syncthreads_and(ok);
+    if (!ok && warp == 0) (void)mbar_wait(bar_in, 0);  // no copy outlives the CTA
     ok = ok && mbar_wait(bar_mma, 0);
     fence_after_sync();
     if (BWD) {  // 2^g q, before A takes the tile's place
@@ -683,6 +684,7 @@ __device__ __forceinline__ void chain_body(const CUtensorMap* tm_q, const CUtens
     // 512 threads x 128 registers at launch = 2 x 128 x 176 + 128 x 96 + 128 x 64
     if (kOut && warp >= 12) regs_dec<64>();
     if (warp == C::kMmaWarp + 1) {  // loads, two stages
+        int issued = 0;
         for (int it = 0; it < nch && ok; ++it) {
             const int s = it & 1;
             if (it >= 2) ok = warp_wait(bar_empty + 8 * s, (uint32_t)((it >> 1) - 1) & 1u, s_abort);
@@ -704,9 +706,10 @@ __device__ __forceinline__ void chain_body(const CUtensorMap* tm_q, const CUtens
                 }
             }
             __syncwarp();
+            issued = ok ? it + 1 : issued;
         }
-        for (int it = nch > 2 ? nch - 2 : 0; it < nch; ++it)  // no copy outlives the CTA, whatever gave up
-            if (!ok) (void)mbar_wait(bar_full + 8 * (it & 1), (uint32_t)(it >> 1) & 1u);
+        for (int it = issued > 2 ? issued - 2 : 0; it < issued; ++it)  // no copy outlives the CTA, whatever gave up
+            (void)mbar_wait(bar_full + 8 * (it & 1), (uint32_t)(it >> 1) & 1u);
     } else if (warp == C::kMmaWarp) {
         const uint32_t id128m = idesc_bf16(128, 128, false, true), id64 = idesc_bf16(128, 64, false, false),
                        id32 = idesc_bf16(128, 32, false, false), id64m = idesc_bf16(128, 64, false, true),
@@ -1071,7 +1074,8 @@ __device__ __forceinline__ void join_body(const ChainArgs& ca, const Segments& s
 #pragma unroll
         for (int k = 0; k < 64; ++k) S[k] = src[(size_t)k * 128];
         float* dst = sg.F + at(g) + (size_t)(16 * warp) * 128 + v;
-        const bool ok = mbar_wait(bar, (uint32_t)i & 1u);
+        const uint32_t par = (uint32_t)i & 1u;
+        const bool ok = mbar_wait(bar, par);
 #pragma unroll 1
         for (int r = 0; r < 16; r += 4) {
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1098,7 +1102,10 @@ __device__ __forceinline__ void join_body(const ChainArgs& ca, const Segments& s
                 if (ok && lane < 16) dst[(size_t)(r + e) * 128] += acc[e];
             }
         }
-        __syncthreads();  // M consumed, F' visible to the CTA
+        if (!__syncthreads_and(ok)) {  // M consumed, F' visible to the CTA
+            (void)mbar_wait(bar, par);  // the copy does not outlive the CTA
+            break;
+        }
     }
 }
 

@@ -391,7 +391,8 @@ kda_status kda_gdn_decode_step(const void* q, const void* k, const void* v, cons
  *   slots  [N] int32 on the device: the slot of each state.
  * Write: scale = max |row| / 127, code = row / scale rounded to the nearest integer, ties to even (both
  * divisions IEEE fp32); a row of zeros has scale 0; a row that holds an infinity or a NaN has scale NaN.
- * Read: S = code * scale.  So a finite value comes back within scale / 2.
+ * Read: S = code * scale.  So a value of a finite row comes back within scale / 2, up to the rounding of
+ * the product; where the largest is below 2^-119 the scale itself is a denormal and adds 2^-142.
  * A negative slot is "none": write skips that state and read returns zeros for it.  A slot >= num_slots
  * does the same and records KDA_ERR_INVALID_ARG for kda_check().  Where `slots` names a slot twice, write
  * keeps the state that comes later; read may name one as often as it likes.  Other slots are untouched.
