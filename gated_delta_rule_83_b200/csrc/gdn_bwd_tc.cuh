@@ -375,6 +375,12 @@ constexpr int kGThreads = 256;
 constexpr uint32_t kGS = 0, kGU = 65536, kGDr = 98304, kGK = 131072, kGQ = 147456, kGDo = 163840, kGV = 180224,
                    kGPd = kGDo, kGG = kGV, kGMisc = 196608, kGSmem = kGMisc + 8192 + 1024;
 
+constexpr unsigned kGAhead = 148;  // one CTA an SM
+
+__device__ __forceinline__ void bulk_prefetch(const void* p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void grad_ld32(uint32_t taddr, float* x)
 {
     tmem_ld16_pair<64>(taddr, x);
@@ -426,6 +432,12 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         bulk_g2s(sb + kGU, img + kImgU, 65536, bar_in);  // U and dR
         bulk_g2s(sb + kGS, img + kImgS, 65536, bar_s);
+        // dS' and the images of the unit that will run here next into L2, while this one computes
+        bulk_prefetch(img + kImgDs, 65536);
+        if (blockIdx.x + kGAhead < gridDim.x) {
+            bulk_prefetch(img + (size_t)kGAhead * kImages + kImgS, 65536);
+            bulk_prefetch(img + (size_t)kGAhead * kImages + kImgU, 65536);
+        }
     }
     if (warp == 1) load_scalars(la, beta, t0, L, H, h, s_g, s_gl, s_b);
     if (warp == 2) {
