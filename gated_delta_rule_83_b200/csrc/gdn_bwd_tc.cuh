@@ -363,9 +363,9 @@ gdn_bwd_chains_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 // Gradients of one (chunk, head): all products M = 64 (row = token), 256 threads.
 //   first:  dO S^T and dR S^T (N = 128); dO U^T, dR U^T, k k^T and v dR^T (N = 64; of the last the diagonal)
 //   then, with dS' in S's place and the split PD and G in dO's and v's:  U dS'^T, PD k, G k, PD^T q + G^T k
-// 192 KB of operands, one CTA an SM; bound by their loads and the tensor pipe in turn: 32K tokens x 32 heads
-// 1.21 ms, 4.3 GB at 0.55 of the copy bandwidth, tensor pipe 43 % busy.  Half the operands in flight at a time and
-// two CTAs an SM do not fit: TMEM has 512 columns and one CTA fills them.
+// 192 KB of operands and all of TMEM, one CTA an SM, so loads, MMAs and the conversions of a unit alternate: 32K
+// tokens x 32 heads 1.13 ms, 4.3 GB at 0.59 of the copy bandwidth, tensor pipe 45 % busy.  Fetching dS' and the next
+// unit's images into L2 ahead took it there from 1.21; all of the next unit's operands cost 1.20..1.30.
 // TMEM columns: 0 dO S^T, 128 dR S^T, 256 dO U^T, 320 dR U^T, 384 k k^T, 448 v dR^T; then 0 U dS'^T, 128 PD k,
 // 256 G k, 384 PD^T q + G^T k.
 // A thread holds 32 channels of a token row: row 16 (warp % 4) + lane % 16, channels 64 (lane / 16) +
@@ -432,12 +432,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         bulk_g2s(sb + kGU, img + kImgU, 65536, bar_in);  // U and dR
         bulk_g2s(sb + kGS, img + kImgS, 65536, bar_s);
-        // dS' and the images of the unit that will run here next into L2, while this one computes
-        bulk_prefetch(img + kImgDs, 65536);
-        if (blockIdx.x + kGAhead < gridDim.x) {
-            bulk_prefetch(img + (size_t)kGAhead * kImages + kImgS, 65536);
-            bulk_prefetch(img + (size_t)kGAhead * kImages + kImgU, 65536);
-        }
+        bulk_prefetch(img + kImgDs, 65536);  // into L2 already
     }
     if (warp == 1) load_scalars(la, beta, t0, L, H, h, s_g, s_gl, s_b);
     if (warp == 2) {
@@ -554,6 +549,10 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (ok && elect_one()) {
             mbar_arrive_expect_tx(bar_ds, 65536);
             bulk_g2s(sb + kGS, img + kImgDs, 65536, bar_ds);
+            if (blockIdx.x + kGAhead < gridDim.x) {  // L2 takes what the unit that runs here next starts on
+                bulk_prefetch(img + (size_t)kGAhead * kImages + kImgS, 65536);
+                bulk_prefetch(img + (size_t)kGAhead * kImages + kImgU, 65536);
+            }
         }
         __syncwarp();
     }
