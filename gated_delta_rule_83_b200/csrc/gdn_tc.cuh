@@ -154,7 +154,7 @@ constexpr uint32_t kImgS = 0, kImgDs = 65536, kImgU = 131072, kImgDr = 163840, k
 // cores: the product form's powers of A would lose the small entries, and the split images need X to 16
 // bits.  Y is a split M = 64 product.  Bound by that dependent chain's latency and its shared-memory accesses, so
 // CTAs are kept small (57 KB, 64 registers) to run four an SM: A lies where Y will, over the consumed [k; q]
-// tile.  32K tokens x 32 heads: 310 us (shared-memory pipe 77 % busy, issue slots 49 %, DRAM 30 %); 4 x 4 tiles
+// tile.  32K tokens x 32 heads: 310 us (shared-memory pipe 70 % busy, issue slots 52 %, DRAM 23 %); 4 x 4 tiles
 // in the last merge 313; larger tiles and three CTAs an SM cost 401 against 347 when that was changed.
 // ----------------------------------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;

@@ -9,9 +9,9 @@
 //
 // Both are one streaming pass: 4 + 1 bytes an element.  A thread moves 8 consecutive values of a row (one
 // 32-byte access to the fp32 side, 8 bytes of codes) and holds kCacheRows rows in flight to cover the memory
-// latency; the state's loads are issued before the slot is known.  Bound by HBM: 192 states of 32 heads, d = 128,
-// read back in 67 us (0.96 of the copy bandwidth); 64 written in 37 us (0.70: the maximum has to be known before
-// the first code) and read in 28.
+// latency; the state's loads are issued before the slot is known.  Bound by HBM: 192 states of 32 heads,
+// d = 128, read back in 67..70 us (0.92..0.96 of the copy bandwidth); 64 written in 37 us (0.70: the maximum has
+// to be known before the first code) and read in 28.
 #pragma once
 
 #include "common.cuh"
