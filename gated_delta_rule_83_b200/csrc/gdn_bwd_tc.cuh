@@ -10,6 +10,10 @@
 //     dbeta_i = dR_i.v_i - 2^g_i k_i.(dR S^T)_i + (E . k k^T) row sum
 //     dg_i = q_i.dq_i + k_i.ka_i - k_i.kb_i,  dg_C += sum_j w_j k_j.(U dS'^T)_j + 2^g_C <S, dS'>
 //     dlog_alpha_i = sum of dg_m over m >= i in the chunk
+// of which PD's diagonal cancels in each dg_i and the terms of w and U with the sum at C; they are left out, so that
+// a gate that acts on a zero state has a gradient of zero (not of 1e-6):
+//     dlog_alpha_i = sum over m >= i of [q.dq + k.ka - k.kb without them]_m + sum over m < i of w_m k_m.(U dS'^T)_m
+//                    + 2^g_C <S, dS'>
 // Three passes: per-chunk matrices (gdn_prep); side by side the forward states again and the reverse chain
 // for dS' and dR (in segments, with a pass for their ends before); one CTA a (chunk, head) for the gradients.
 // dg is taken from row products of terms that belong to this chunk, never from a sum over the whole sequence,
@@ -409,6 +413,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     float* s_gl = s_g + 128;                              // [64]
     float* s_red = s_g + 192;                             // [4 sums][4 parts][64 rows]
     float* s_sds = s_red + 1024;                          // [8]
+    float* s_pd = s_sds + 8;                              // [64] diagonal of PD
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + kGMisc + 6144);
     const uint32_t bar_in = sb + kGMisc + 6160, bar_s = bar_in + 8, bar_ds = bar_in + 16, bar_read = bar_in + 24,
                    bar_m = bar_in + 32;  // 4 MMA barriers
@@ -528,7 +533,8 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         for (int m = 0; m < 16; ++m) {
             const int j = j0 + m;
             const float D = ex2_approx((gi - s_g[j]) + (gli - s_gl[j]));
-            x[m] = (j <= r && r < L) ? x[m] * D : 0.f;
+            if (j == r) s_pd[r] = r < L ? x[m] : 0.f;
+            x[m] = (j < r && r < L) ? x[m] * D : 0.f;
             const float e = (j < r && r < L) ? -y[m] * D : 0.f;
             db = fmaf(e, z[m], db);
             if (j == r) db += v[m];
@@ -636,6 +642,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     fence_after_sync();
     const bool row = r < L && c0 < dkw && ok;
     const size_t orow = ((size_t)(t0 + r) * H + h) * dkw + c0;
+    const float pd = s_pd[r];
     float dot = 0.f;
     {
         float x[32];
@@ -655,6 +662,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         for (int e = 0; e < 8; ++e) {
             dot = fmaf(q8[e], rq[8 * b + e], dot);
             dot = fmaf(k8[e], ra[8 * b + e], dot);
+            rq[8 * b + e] = fmaf(pd, k8[e], rq[8 * b + e]);
         }
         if (row) {
             if (dq_acc) {
@@ -674,15 +682,16 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         grad_ld32(tl + 384 + 32 * hw, y);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            float k8[8];
+            float q8[8], k8[8];
+            unpack8(*reinterpret_cast<const uint4*>(sm + kGQ + sw128_chunk_off(r, (c0 >> 3) + b, 64)), q8);
             unpack8(*reinterpret_cast<const uint4*>(sm + kGK + sw128_chunk_off(r, (c0 >> 3) + b, 64)), k8);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int m = 8 * b + e;
-                const float a = wi * x[m], kb = a + y[m];
+                const float a = wi * x[m];
                 kw = fmaf(k8[e], a, kw);
-                dot = fmaf(-k8[e], kb, dot);
-                ra[m] += kb;
+                dot = fmaf(-k8[e], y[m], dot);
+                ra[m] += fmaf(pd, q8[e], a + y[m]);
             }
             if (row && ok) {
                 if (dk_acc) {
@@ -713,31 +722,29 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const float* p = s_red + 256 * k + i;
             return (p[0] + p[64]) + (p[128] + p[192]);
         };
-        float a0 = sum4(0, 2 * lane), a1 = sum4(0, 2 * lane + 1);
-        float c = sum4(1, 2 * lane) + sum4(1, 2 * lane + 1);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-        if (lane == 31) {
-            float t = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) t += s_sds[i];
-            a1 += c + ex2_approx(s_g[63]) * t;
-        }
-        float s = a0 + a1;  // sums over the tokens behind
+        // dlog_alpha_i = sum of dot_m over m >= i  +  sum of kw_m over m < i  +  2^g_C <S, dS'>
+        const float a0 = sum4(0, 2 * lane), a1 = sum4(0, 2 * lane + 1), k0 = sum4(1, 2 * lane), k1 = sum4(1, 2 * lane + 1);
+        float s = a0 + a1, c = k0 + k1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float y = __shfl_down_sync(0xffffffffu, s, o);
+            const float y = __shfl_down_sync(0xffffffffu, s, o), z = __shfl_up_sync(0xffffffffu, c, o);
             if (lane + o < 32) s += y;
+            if (lane >= o) c += z;
         }
-        float behind = __shfl_down_sync(0xffffffffu, s, 1);
+        float behind = __shfl_down_sync(0xffffffffu, s, 1), ahead = __shfl_up_sync(0xffffffffu, c, 1);
         if (lane == 31) behind = 0.f;
+        if (lane == 0) ahead = 0.f;
+        float end = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) end += s_sds[i];
+        end *= ex2_approx(s_g[63]);
         const size_t o = (size_t)(t0 + 2 * lane) * H + h;
         if (2 * lane < L) {
-            dla[o] = s;
+            dla[o] = (s + ahead) + end;
             dbeta[o] = sum4(2, 2 * lane);
         }
         if (2 * lane + 1 < L) {
-            dla[o + H] = behind + a1;
+            dla[o + H] = (behind + a1) + (ahead + k0) + end;
             dbeta[o + H] = sum4(2, 2 * lane + 1);
         }
     }

@@ -281,6 +281,17 @@ def test_tokens_that_forget_all(dt, d_, gate):
         check(g[x], ref[x], dt, x)
 
 
+@pytest.mark.parametrize("dk,dv,kw", [(128, 128, dict(lens=[1] * 5)), (64, 128, dict(T=1, B=3))])
+def test_a_gate_on_a_zero_state_has_no_gradient(dk, dv, kw):
+    """Sequences of one token and no start state: log_alpha multiplies zeros, so its gradient is exactly
+    zero; with a start state it is alpha <(I - beta k k^T) S0, dS> alone, small where S0 is."""
+    d = make(31, torch.bfloat16, 4, 2, dk, dv, s0=False, **kw)
+    assert not run_bwd(d)["dlog_alpha"].any()
+    d = make(32, torch.bfloat16, 4, 2, dk, dv, **kw)
+    d["S0"] *= 2.0 ** -7
+    check(run_bwd(d)["dlog_alpha"], ref_bwd(d)["dlog_alpha"], torch.bfloat16, "dlog_alpha")
+
+
 def test_sequences_do_not_see_their_neighbours():
     """Packed input in which one sequence holds NaN and infinities throughout, cotangents too: the others get
     the very numbers they get without it."""
