@@ -167,7 +167,8 @@ extern "C" kda_status kda_gdn_chunk_bwd(const void* q, const void* k, const void
                                         dv_out, dgate, dbeta, dS0, B, T, H, dk, dv, dt, &opt, workspace,
                                         p.b.total_bytes, stream_);
     if (sb != KDA_OK) return sb;
-    if (Ttot > 0 && launch_gdn_sum_gate(dgate, dlog_alpha, Ttot * H, dk, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    if (Ttot > 0 && launch_gdn_sum_gate(dgate, dlog_alpha, Ttot * H, dk, H, (const WsHeader*)workspace, cu_seqlens, p.b.f.Tseq,
+                                        p.b.f.N, S0 != nullptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
     return KDA_OK;
 }
 

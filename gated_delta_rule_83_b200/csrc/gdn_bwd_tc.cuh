@@ -754,10 +754,11 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 // A stream of fp32 rows: 33 us for 8192 tokens x 16 value heads.
 __global__ void __launch_bounds__(256)
 gdn_bwd_heads_kernel(const float* __restrict__ dq_acc, const float* __restrict__ dk_acc, __nv_bfloat16* __restrict__ dq,
-                     __nv_bfloat16* __restrict__ dk, long long quads, int G, int w)
+                     __nv_bfloat16* __restrict__ dk, long long quads, int G, int w, const WsHeader* __restrict__ hdr,
+                     const int32_t* __restrict__ cu)
 {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= quads) return;
+    if (i >= quads || (cu && hdr->bad)) return;
     const long long row = i / w;
     const int c = (int)(i - row * w);
     const float4* acc = reinterpret_cast<const float4*>(blockIdx.y ? dk_acc : dq_acc) + row * G * w + c;
@@ -852,7 +853,7 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
         const long long quads = Ttot * Hk * (dkw / 4), blocks = (quads + 255) / 256;
         if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
         gdn_bwd_heads_kernel<<<dim3((unsigned)blocks, 2), 256, 0, stream>>>(
-            dq_acc, dk_acc, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, quads, H / Hk, dkw / 4);
+            dq_acc, dk_acc, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, quads, H / Hk, dkw / 4, hdr, cu);
         e = cudaGetLastError();
     }
     return e;

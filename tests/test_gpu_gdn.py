@@ -281,15 +281,16 @@ def test_tokens_that_forget_all(dt, d_, gate):
         check(g[x], ref[x], dt, x)
 
 
-@pytest.mark.parametrize("dk,dv,kw", [(128, 128, dict(lens=[1] * 5)), (64, 128, dict(T=1, B=3))])
-def test_a_gate_on_a_zero_state_has_no_gradient(dk, dv, kw):
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dk,dv,kw", [(128, 128, dict(lens=[1, 1, 0, 1, 1])), (64, 128, dict(T=1, B=3))])
+def test_a_gate_on_a_zero_state_has_no_gradient(dt, dk, dv, kw):
     """Sequences of one token and no start state: log_alpha multiplies zeros, so its gradient is exactly
     zero; with a start state it is alpha <(I - beta k k^T) S0, dS> alone, small where S0 is."""
-    d = make(31, torch.bfloat16, 4, 2, dk, dv, s0=False, **kw)
+    d = make(31, dt, 4, 2, dk, dv, s0=False, **kw)
     assert not run_bwd(d)["dlog_alpha"].any()
-    d = make(32, torch.bfloat16, 4, 2, dk, dv, **kw)
+    d = make(32, dt, 4, 2, dk, dv, **kw)
     d["S0"] *= 2.0 ** -7
-    check(run_bwd(d)["dlog_alpha"], ref_bwd(d)["dlog_alpha"], torch.bfloat16, "dlog_alpha")
+    check(run_bwd(d)["dlog_alpha"], ref_bwd(d)["dlog_alpha"], dt, "dlog_alpha")
 
 
 def test_sequences_do_not_see_their_neighbours():
@@ -390,6 +391,22 @@ def test_bad_offsets_are_reported_and_nothing_is_written(bad):
         m.check()
     assert e.value.code == 6
     assert (out == 3.0).all() and (S == 3.0).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_bad_offsets_leave_the_gradients(dt):
+    m = kda()
+    d = make(12, dt, 2, 1, 128, 128, lens=[30, 30, 40])
+    d["cu"] = torch.tensor([0, 50, 40, 100], dtype=torch.int32, device=DEV)
+    mine = {x: torch.full_like(d[y], 3.0) for x, y in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dS0", "S0"),
+                                                       ("dlog_alpha", "log_alpha"), ("dbeta", "beta"))}
+    m.gdn_chunk_bwd(d["q"], d["k"], d["v"], d["log_alpha"], d["beta"], d["dout"], S0=d["S0"], cu_seqlens=d["cu"],
+                    grads=mine)
+    with pytest.raises(m.KdaError) as e:
+        m.check()
+    assert e.value.code == 6
+    for x in ("dv", "dS0", "dlog_alpha", "dbeta") + (("dq", "dk") if dt == torch.bfloat16 else ()):
+        assert (mine[x] == 3.0).all(), x  # (in fp32 the sum over shared heads writes dq and dk)
 
 
 def test_binding_refuses():
