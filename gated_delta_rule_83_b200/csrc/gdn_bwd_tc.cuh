@@ -368,8 +368,8 @@ gdn_bwd_chains_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 //   first:  dO S^T and dR S^T (N = 128); dO U^T, dR U^T, k k^T and v dR^T (N = 64; of the last the diagonal)
 //   then, with dS' in S's place and the split PD and G in dO's and v's:  U dS'^T, PD k, G k, PD^T q + G^T k
 // 192 KB of operands and all of TMEM, one CTA an SM, so loads, MMAs and the conversions of a unit alternate: 32K
-// tokens x 32 heads 1.13 ms, 4.3 GB at 0.59 of the copy bandwidth, tensor pipe 44 % busy.  Fetching dS' and the next
-// unit's images into L2 ahead took it there from 1.21; all of the next unit's operands cost 1.20..1.30.
+// tokens x 32 heads 1.15 ms, 4.3 GB at 0.58 of the copy bandwidth, tensor pipe 44 % busy.  Fetching dS' and the next
+// unit's images into L2 ahead saves 0.08; all of the next unit's operands cost 0.06..0.16 instead.
 // TMEM columns: 0 dO S^T, 128 dR S^T, 256 dO U^T, 320 dR U^T, 384 k k^T, 448 v dR^T; then 0 U dS'^T, 128 PD k,
 // 256 G k, 384 PD^T q + G^T k.
 // A thread holds 32 channels of a token row: row 16 (warp % 4) + lane % 16, channels 64 (lane / 16) +
