@@ -35,6 +35,9 @@
 // forward; a tile whose in-chunk gate spread exceeds kFactorSpread takes the exact per-element
 // factor e^{g_r - g_i} (never above 1) instead.  Padding rows of a partial chunk are identity
 // steps with zero inputs and zero cotangents, so they contribute nothing.
+//
+// HEAD (one forget gate a head, fp32): the decays multiply the plain products k k^T and, for dq, dk and dg, the
+// matrices dP and dAt, with g as a pair of floats; dlog_alpha is written for each channel and summed afterwards.
 #pragma once
 
 #include "common.cuh"
@@ -528,7 +531,7 @@ __device__ void bwd_ut_step4a_tc(const __nv_bfloat16* __restrict__ k, const __nv
 // Step 4, first half (one CTA per (chunk, head)): At and dT over all channel and value tiles, the
 // UT transform backwards (N, dbeta, dM -> dAt) and dV.  N and dAt go to the unit's scratch (over U
 // and dU, both dead by then) for the second half.
-template <typename TIn, bool TC>
+template <typename TIn, bool TC, bool HEAD = false>
 __global__ void __launch_bounds__(kSimtThreads, 2)
 bwd_ut_kernel(const TIn* __restrict__ k, const TIn* __restrict__ v, const void* __restrict__ log_alpha,
               const float* __restrict__ beta, const WsHeader* __restrict__ hdr, const int* __restrict__ off,
@@ -559,6 +562,7 @@ bwd_ut_kernel(const TIn* __restrict__ k, const TIn* __restrict__ v, const void* 
     float* sdb = sb + kChunk;     // [64] dbeta
     float* tref = sdb + kChunk;   // [32]
     __shared__ int s_wide;
+    __shared__ __align__(8) float s_g[HEAD ? kChunk : 2], s_gl[HEAD ? kChunk : 2];
 
     const size_t u = (size_t)j * H + h;
     float* o = scr + u * bwd_scr_floats(dk, dv);
@@ -566,7 +570,11 @@ bwd_ut_kernel(const TIn* __restrict__ k, const TIn* __restrict__ v, const void* 
     const float* gdW = gdU + (size_t)kChunk * dv + (size_t)kChunk * dk;
     const int tr = tid >> 4, tc = tid & 15;
 
-    for (int r = tid; r < kChunk; r += kSimtThreads) sb[r] = (r < L) ? beta[(size_t)(t0 + r) * H + h] : 0.f;
+    if constexpr (HEAD) {
+        if (tid < 32) load_scalars(reinterpret_cast<const float*>(log_alpha), beta, t0, L, H, h, s_g, s_gl, sb);
+    } else {
+        for (int r = tid; r < kChunk; r += kSimtThreads) sb[r] = (r < L) ? beta[(size_t)(t0 + r) * H + h] : 0.f;
+    }
 
     // ---- step 4a: At and dT = dW Kt^T + dU V^T, accumulated in registers over tiles
     float accA[4][4] = {}, accT[4][4] = {};
@@ -579,12 +587,16 @@ bwd_ut_kernel(const TIn* __restrict__ k, const TIn* __restrict__ v, const void* 
             if (tid == 0) s_wide = 0;
             __syncthreads();
             bwd_load_tile(k, t0, L, Hk, h / (H / Hk), dk, c0, tk);  // the q/k head of value head h
-            bwd_gate_tile(log_alpha, la16, t0, L, H, h, dk, c0, tg, tref, &s_wide);
+            if constexpr (!HEAD) bwd_gate_tile(log_alpha, la16, t0, L, H, h, dk, c0, tg, tref, &s_wide);
             bwd_load_scr_tile(gdW, dk, c0, tD);
             __syncthreads();
             const bool wide = s_wide != 0;
             for (int e = tid; e < kChunk * kBwdCT; e += kSimtThreads) {
                 const int r = e / kBwdCT, cc = e % kBwdCT;
+                if constexpr (HEAD) {
+                    tC[r * LT + cc] = tk[r * LT + cc] * tc::ex2_approx(s_g[r]);  // Kt; Kf and Kb are k
+                    continue;
+                }
                 const float g = tg[r * LT + cc], x = g - tref[cc], kv = tk[r * LT + cc];
                 tA[r * LT + cc] = wide ? 0.f : kv * fast_exp(x);   // Kf
                 tB[r * LT + cc] = wide ? 0.f : kv * fast_exp(-x);  // Kb
@@ -592,7 +604,7 @@ bwd_ut_kernel(const TIn* __restrict__ k, const TIn* __restrict__ v, const void* 
             }
             __syncthreads();
             if (!wide) {
-                mm_acc<4, 4>(accA, tA, LT, 1, tB, 1, LT, kBwdCT, tr, tc);
+                mm_acc<4, 4>(accA, HEAD ? tk : tA, LT, 1, HEAD ? tk : tB, 1, LT, kBwdCT, tr, tc);
             } else {
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
@@ -620,6 +632,7 @@ bwd_ut_kernel(const TIn* __restrict__ k, const TIn* __restrict__ v, const void* 
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int r = tr + 16 * a, i = tc + 16 * b;
+                if constexpr (HEAD) accA[a][b] *= head_decay(s_g, s_gl, r, i);
                 sAt[r * L64 + i] = (i < r) ? accA[a][b] : 0.f;
                 sM[r * L64 + i] = (i <= r) ? accT[a][b] : 0.f;
             }
@@ -715,7 +728,7 @@ bwd_ut_kernel(const TIn* __restrict__ k, const TIn* __restrict__ v, const void* 
 
 // Step 4, second half (one CTA per (chunk, head, 32-channel tile)): dq, dk and dlog_alpha through
 // the gated products P = Qf Kb^T, At = Kf Kb^T and the gating itself.
-template <typename TIn>
+template <typename TIn, bool HEAD = false>
 __global__ void __launch_bounds__(kSimtThreads, 2)
 bwd_gate_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const void* __restrict__ log_alpha,
                 const float* __restrict__ beta, const WsHeader* __restrict__ hdr, const int* __restrict__ off,
@@ -746,6 +759,7 @@ bwd_gate_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const void
     float* sb = tD + MT;          // [64] beta
     float* tref = sb + kChunk;    // [32]
     __shared__ int s_wide;
+    __shared__ __align__(8) float s_g[HEAD ? kChunk : 2], s_gl[HEAD ? kChunk : 2];
 
     const size_t u = (size_t)j * H + h;
     const float* o = scr + u * bwd_scr_floats(dk, dv);
@@ -769,7 +783,11 @@ bwd_gate_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const void
             pq[a][b] = gdQg[gi];
             pk[a][b] = gdKd[gi];
         }
-    for (int r = tid; r < kChunk; r += kSimtThreads) sb[r] = (r < L) ? beta[(size_t)(t0 + r) * H + h] : 0.f;
+    if constexpr (HEAD) {
+        if (tid < 32) load_scalars(reinterpret_cast<const float*>(log_alpha), beta, t0, L, H, h, s_g, s_gl, sb);
+    } else {
+        for (int r = tid; r < kChunk; r += kSimtThreads) sb[r] = (r < L) ? beta[(size_t)(t0 + r) * H + h] : 0.f;
+    }
     for (int e = tid; e < kChunk * kChunk / 8; e += kSimtThreads) {
         float fn[8], fa[8], fp[8];
         load8(gN + 8 * e, fn);
@@ -787,10 +805,19 @@ bwd_gate_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const void
     bwd_load_tile(q, t0, L, Hk, h / (H / Hk), dk, c0, tq);
     bwd_load_scr_tile(gdW, dk, c0, tD);
     __syncthreads();  // s_wide zeroed before the gate tile flags it
-    bwd_gate_tile(log_alpha, la16, t0, L, H, h, dk, c0, tg, tref, &s_wide);
+    if constexpr (HEAD) {  // dP and dAt with the decays; Kf, Kb and Qf are k and q
+        for (int e = tid; e < kChunk * kChunk; e += kSimtThreads) {
+            const int r = e / kChunk, i = e % kChunk;
+            const float D = i <= r ? head_decay(s_g, s_gl, r, i) : 0.f;
+            sM[r * L64 + i] *= D;
+            sdP[r * L64 + i] *= D;
+        }
+    } else {
+        bwd_gate_tile(log_alpha, la16, t0, L, H, h, dk, c0, tg, tref, &s_wide);
+    }
     __syncthreads();
     const bool wide = s_wide != 0;
-    if (!wide)
+    if (!wide && !HEAD)
         for (int e = tid; e < kChunk * kBwdCT; e += kSimtThreads) {
             const int r = e / kBwdCT, cc = e % kBwdCT;
             const float x = tg[r * LT + cc] - tref[cc];
@@ -804,10 +831,11 @@ bwd_gate_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const void
     // col = sum_a (dP[a][r] q_a + dAt[a][r] k_a) E(a,r), dKt = beta_r sum_a N[a][r] dW[a]
     float rowP[4][2] = {}, rowA[4][2] = {}, col[4][2] = {}, dkt[4][2] = {};
     if (!wide) {
-        mm_acc<4, 2>(rowP, sdP, L64, 1, tB, LT, 1, kChunk, tr, tc);
-        mm_acc<4, 2>(rowA, sM, L64, 1, tB, LT, 1, kChunk, tr, tc);
-        mm_acc<4, 2>(col, sdP, 1, L64, tC, LT, 1, kChunk, tr, tc);
-        mm_acc<4, 2>(col, sM, 1, L64, tA, LT, 1, kChunk, tr, tc);
+        const float *kf = HEAD ? tk : tA, *kb = HEAD ? tk : tB, *qf = HEAD ? tq : tC;
+        mm_acc<4, 2>(rowP, sdP, L64, 1, kb, LT, 1, kChunk, tr, tc);
+        mm_acc<4, 2>(rowA, sM, L64, 1, kb, LT, 1, kChunk, tr, tc);
+        mm_acc<4, 2>(col, sdP, 1, L64, qf, LT, 1, kChunk, tr, tc);
+        mm_acc<4, 2>(col, sM, 1, L64, kf, LT, 1, kChunk, tr, tc);
     } else {
 #pragma unroll
         for (int a = 0; a < 4; ++a)
@@ -832,8 +860,8 @@ bwd_gate_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const void
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int r = tr + 16 * a, cc = tc + 16 * b;
-            const float g = tg[r * LT + cc], gl = tg[(kChunk - 1) * LT + cc];
-            if (!wide) {
+            const float g = HEAD ? 0.f : tg[r * LT + cc], gl = HEAD ? 0.f : tg[(kChunk - 1) * LT + cc];
+            if (!wide && !HEAD) {
                 const float x = g - tref[cc];
                 const float ex = fast_exp(x);
                 rowP[a][b] *= ex;
@@ -841,7 +869,8 @@ bwd_gate_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const void
                 col[a][b] *= fast_exp(-x);
             }
             const float kt = dkt[a][b] * sb[r];
-            const float eg = fast_exp(g), egl = fast_exp(gl - g);
+            const float eg = HEAD ? tc::ex2_approx(s_g[r]) : fast_exp(g),
+                        egl = HEAD ? head_decay(s_g, s_gl, kChunk - 1, r) : fast_exp(gl - g);
             const float qv = tq[r * LT + cc], kv = tk[r * LT + cc];
             const float dQg = pq[a][b], dKd = pk[a][b];
             const float vq = rowP[a][b] + dQg * eg;
@@ -874,7 +903,7 @@ bwd_gate_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const void
         const int cc = tid;
         float s = 0.f;
         for (int r = 0; r < kChunk; ++r) s += tA[r * LT + cc];
-        s += gdGam[c0 + cc] * fast_exp(tg[(kChunk - 1) * LT + cc]);
+        s += gdGam[c0 + cc] * (HEAD ? tc::ex2_approx(s_g[kChunk - 1]) : fast_exp(tg[(kChunk - 1) * LT + cc]));
         float acc = s;
         for (int r = kChunk - 1; r >= 0; --r) {
             acc += tB[r * LT + cc];
@@ -1070,7 +1099,7 @@ cudaError_t launch_bwd_chains(const float* S0, const void* dout, const float* dS
 // Steps 1-4.  Workspace regions (all per (chunk, head) of the forward's chunk table): the
 // CUDA-core forward slots, chunk start states, chunk end cotangents and the per-chunk scratch.
 
-template <typename TIn>
+template <typename TIn, bool HEAD = false>
 cudaError_t launch_simt_backward(const void* q, const void* k, const void* v, const void* la, const float* beta,
                                  const float* S0, const void* dout, const float* dS_final, void* dq, void* dk_out,
                                  void* dv_out, float* dla, float* dbeta, float* dS0, const WsHeader* hdr,
@@ -1113,18 +1142,19 @@ cudaError_t launch_simt_backward(const void* q, const void* k, const void* v, co
     const size_t smA = simt_intra_smem(dk, dv), smS = bwd_state_side_smem(dk, dv), smU = bwd_ut_smem(),
                  smG = bwd_gate_smem();
     const bool tcr = bwd_state_side_tc_ok(sizeof(TIn) == 2, dk, dv);  // the recompute's products on tcgen05
-    auto* kintra = tcr ? simt_intra_kernel<TIn, sizeof(TIn) == 2> : simt_intra_kernel<TIn, false>;
+    static_assert(!HEAD || sizeof(TIn) == 4, "bf16 with one gate a head has kernels of its own");
+    auto* kintra = tcr ? simt_intra_kernel<TIn, sizeof(TIn) == 2, HEAD> : simt_intra_kernel<TIn, false, HEAD>;
     const size_t smAk = smA + (tcr ? 1024 : 0);
     cudaError_t e = cudaFuncSetAttribute(kintra, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smAk);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(bwd_state_side_kernel<TIn>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smS);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(bwd_ut_kernel<TIn, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smU);
+        e = cudaFuncSetAttribute(bwd_ut_kernel<TIn, false, HEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smU);
     if (e == cudaSuccess && sizeof(TIn) == 2)
-        e = cudaFuncSetAttribute(bwd_ut_kernel<TIn, sizeof(TIn) == 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(bwd_ut_kernel<TIn, sizeof(TIn) == 2, HEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smU);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(bwd_gate_kernel<TIn>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smG);
+        e = cudaFuncSetAttribute(bwd_gate_kernel<TIn, HEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smG);
     if (e != cudaSuccess) return e;
     const TIn *qq = (const TIn*)q, *kk = (const TIn*)k, *vv = (const TIn*)v;
     if (max_chunks > 0) {
@@ -1154,7 +1184,7 @@ cudaError_t launch_simt_backward(const void* q, const void* k, const void* v, co
         {
             const bool tc = bwd_state_side_tc_ok(sizeof(TIn) == 2, dk, dv);
             LaunchScope ls(tc ? "bwd_ut_tc" : "bwd_ut", stream);
-            auto* kut = tc ? bwd_ut_kernel<TIn, sizeof(TIn) == 2> : bwd_ut_kernel<TIn, false>;
+            auto* kut = tc ? bwd_ut_kernel<TIn, sizeof(TIn) == 2, HEAD> : bwd_ut_kernel<TIn, false, HEAD>;
             kut<<<dim3(max_chunks, H), kSimtThreads, smU, stream>>>(
                 kk, vv, la, beta, hdr, off, cu, Tseq, N, H, Hk, pro & KDA_PROLOGUE_GATE_BF16, dk, dv, scr,
                 (TIn*)dv_out, dbeta);
@@ -1167,7 +1197,7 @@ cudaError_t launch_simt_backward(const void* q, const void* k, const void* v, co
             if (e != cudaSuccess) return e;
         } else {
             LaunchScope ls("bwd_gate", stream);
-            bwd_gate_kernel<TIn><<<dim3(max_chunks, H, dk / kBwdCT), kSimtThreads, smG, stream>>>(
+            bwd_gate_kernel<TIn, HEAD><<<dim3(max_chunks, H, dk / kBwdCT), kSimtThreads, smG, stream>>>(
                 qq, kk, la, beta, hdr, off, cu, Tseq, N, H, Hk, pro & KDA_PROLOGUE_GATE_BF16, dk, dv, scr, (TIn*)dq,
                 (TIn*)dk_out, dla, (grouped || l2norm) ? dq_acc : nullptr, (grouped || l2norm) ? dk_acc : nullptr);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;

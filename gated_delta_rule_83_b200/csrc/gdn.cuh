@@ -1,25 +1,14 @@
 // gdn.cuh -- the gated delta rule with one forget gate a head, on the CUDA-core chunk kernels.
 //
-// fp32 inputs run here.  The per-channel kernels hold the scalar gate as the special case of equal channels,
-// so the gate is spread over the dk channels into the workspace, and in the backward the channels' gate
-// gradients are summed.  Both are streams; a call of a few hundred tokens is a chain of launches (69 us the
-// prefill, 159 us the backward).
+// fp32 inputs run there, in instances of the per-channel form's kernels that take the decays of a head in place of
+// the channels' (head_gate.cuh).  The backward leaves the gate's gradient for each key channel; their sum is here.
+// A call of a few hundred tokens is a chain of launches (61 us the prefill, 149 us the backward).
 #pragma once
 
 #include "common.cuh"
 #include "profile.cuh"
 
 namespace kda {
-
-__global__ void __launch_bounds__(256)
-gdn_spread_gate_kernel(const float* __restrict__ la, float4* __restrict__ out, long long n, int quads)
-{
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // a float4 of one (token, head)
-    if (i >= n) return;
-    float a = la[i / quads];
-    a = a < -104.f ? -104.f : a;  // e^-104 rounds every state to zero, and -inf would make differences NaN
-    out[i] = make_float4(a, a, a, a);
-}
 
 // One warp per (token, head): the sum over its dk channels, in a fixed order.  Without a start state the first
 // gate of a sequence multiplies zeros: its gradient is zero, where the channels hold the rounding of terms that
@@ -54,15 +43,6 @@ gdn_sum_gate_kernel(const float* __restrict__ dla, float* __restrict__ out, long
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) out[r] = s;
-}
-
-inline cudaError_t launch_gdn_spread_gate(const float* la, float* out, long long rows, int dk, cudaStream_t stream)
-{
-    LaunchScope ls("gdn_spread_gate", stream);
-    const long long n = rows * (dk / 4), blocks = (n + 255) / 256;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    gdn_spread_gate_kernel<<<(unsigned)blocks, 256, 0, stream>>>(la, (float4*)out, n, dk / 4);
-    return cudaGetLastError();
 }
 
 inline cudaError_t launch_gdn_sum_gate(const float* dla, float* out, long long rows, int dk, int H, const WsHeader* hdr,

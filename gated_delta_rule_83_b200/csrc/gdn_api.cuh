@@ -6,14 +6,14 @@ namespace {
 
 bool gdn_heads_ok(int H, int Hk) { return H > 0 && Hk > 0 && H % Hk == 0; }
 
-// bf16 runs on the tensor cores.  fp32 inputs run on the CUDA-core chunk kernels: split into bf16 parts they
+// bf16 runs on the tensor cores.  fp32 inputs run on the CUDA-core chunk kernels: split into two bf16 parts they
 // would lose eight of their bits.
 bool gdn_use_tc(kda_dtype dt) { return dt == KDA_BF16; }
 
 struct GdnFwdPlan {
     Plan f;
     bool tc;
-    size_t gate_bytes, total;
+    size_t total;
 };
 
 kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, int num_seqs, kda_dtype dt,
@@ -22,8 +22,7 @@ kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, i
     const kda_status st = make_plan(B, T, H, dk, dv, varlen, num_seqs, dt, p.f);
     if (st != KDA_OK) return st;
     p.tc = gdn_use_tc(dt);
-    p.gate_bytes = p.tc ? 0 : round_up(sizeof(float) * (size_t)p.f.Ttot * H * dk, kAlign);
-    p.total = sizeof(WsHeader) + p.f.off_bytes + p.gate_bytes +
+    p.total = sizeof(WsHeader) + p.f.off_bytes +
               (p.tc ? gdn::fwd_bytes(p.f.max_chunks, p.f.N, H)
                     : (size_t)p.f.max_chunks * H * round_up(sizeof(float) * simt_slot_floats(dk, dv), kAlign));
     return KDA_OK;
@@ -32,7 +31,7 @@ kda_status make_gdn_fwd_plan(int B, int T, int H, int dk, int dv, bool varlen, i
 struct GdnBwdPlan {
     BwdPlan b;
     bool tc;
-    size_t gate_bytes, total;
+    size_t total;  // behind the backward's own (fp32): the gate's gradient for each key channel
 };
 
 kda_status make_gdn_bwd_plan(int B, int T, int H, int Hk, int dk, int dv, bool varlen, int num_seqs, kda_dtype dt,
@@ -42,13 +41,11 @@ kda_status make_gdn_bwd_plan(int B, int T, int H, int Hk, int dk, int dv, bool v
     if (st != KDA_OK) return st;
     p.tc = gdn_use_tc(dt);
     if (p.tc) {
-        p.gate_bytes = 0;
         p.total = sizeof(WsHeader) + p.b.f.off_bytes +
                   gdn::bwd_layout(p.b.f.max_chunks, p.b.f.N, p.b.f.Ttot, H, dk, Hk != H).total;
         return KDA_OK;
     }
-    p.gate_bytes = round_up(sizeof(float) * (size_t)p.b.f.Ttot * H * dk, kAlign);
-    p.total = round_up(p.b.total_bytes, kAlign) + 2 * p.gate_bytes;
+    p.total = round_up(p.b.total_bytes, kAlign) + sizeof(float) * (size_t)p.b.f.Ttot * H * dk;
     return KDA_OK;
 }
 
@@ -96,18 +93,12 @@ extern "C" kda_status kda_gdn_chunk_fwd(const void* q, const void* k, const void
                                                             off + p.f.N + 1);
         if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
     }
-    float* gate = (float*)(ws + sizeof(WsHeader) + p.f.off_bytes);
-    float* slots = (float*)((char*)gate + p.gate_bytes);
-    cudaError_t e = cudaSuccess;
-    if (p.tc) {
-        e = gdn::launch_fwd(q, k, v, log_alpha, beta, S0, S_final, out, hdr, off, cu_seqlens, p.f.Tseq, p.f.N, H, Hk,
-                            dk, dv, p.f.max_chunks, p.f.Ttot, (uint8_t*)slots, stream);
-        return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
-    }
-    if (p.f.Ttot > 0) e = launch_gdn_spread_gate(log_alpha, gate, p.f.Ttot * H, dk, stream);
-    if (e == cudaSuccess)
-        e = launch_simt_prefill<float>(q, k, v, gate, beta, S0, S_final, out, hdr, off, cu_seqlens, p.f.Tseq, p.f.N, H, Hk,
-                                       0u, dk, dv, p.f.max_chunks, slots, stream);
+    char* slots = ws + sizeof(WsHeader) + p.f.off_bytes;
+    const cudaError_t e =
+        p.tc ? gdn::launch_fwd(q, k, v, log_alpha, beta, S0, S_final, out, hdr, off, cu_seqlens, p.f.Tseq, p.f.N, H, Hk, dk,
+                               dv, p.f.max_chunks, p.f.Ttot, (uint8_t*)slots, stream)
+             : launch_simt_prefill<float, true>(q, k, v, log_alpha, beta, S0, S_final, out, hdr, off, cu_seqlens,
+                                                p.f.Tseq, p.f.N, H, Hk, 0u, dk, dv, p.f.max_chunks, (float*)slots, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -158,18 +149,14 @@ extern "C" kda_status kda_gdn_chunk_bwd(const void* q, const void* k, const void
                                               (uint8_t*)(ws + sizeof(WsHeader) + f.off_bytes), stream);
         return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
-    float* gate = (float*)((char*)workspace + round_up(p.b.total_bytes, kAlign));
-    float* dgate = (float*)((char*)gate + p.gate_bytes);
-    if (Ttot > 0 && launch_gdn_spread_gate(log_alpha, gate, Ttot * H, dk, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    kda_options opt{};
-    opt.num_qk_heads = Hk;
-    const kda_status sb = kda_chunk_bwd(q, k, v, gate, beta, S0, cu_seqlens, num_seqs, dout, dS_final, dq, dk_out,
-                                        dv_out, dgate, dbeta, dS0, B, T, H, dk, dv, dt, &opt, workspace,
-                                        p.b.total_bytes, stream_);
-    if (sb != KDA_OK) return sb;
-    if (Ttot > 0 && launch_gdn_sum_gate(dgate, dlog_alpha, Ttot * H, dk, H, (const WsHeader*)workspace, cu_seqlens, p.b.f.Tseq,
-                                        p.b.f.N, S0 != nullptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    return KDA_OK;
+    if (!all_aligned16({beta, dbeta})) return KDA_ERR_INVALID_ARG;
+    float* dgate = (float*)((char*)workspace + round_up(p.b.total_bytes, kAlign));
+    cudaError_t e = run_backward<float, true>(q, k, v, log_alpha, beta, S0, cu_seqlens, dout, dS_final, dq, dk_out, dv_out,
+                                              dgate, dbeta, dS0, H, Hk, 0u, dk, dv, p.b, (char*)workspace, stream);
+    if (e == cudaSuccess && Ttot > 0)
+        e = launch_gdn_sum_gate(dgate, dlog_alpha, Ttot * H, dk, H, (const WsHeader*)workspace, cu_seqlens, p.b.f.Tseq,
+                                p.b.f.N, S0 != nullptr, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 extern "C" kda_status kda_gdn_decode_step(const void* q, const void* k, const void* v, const float* log_alpha,

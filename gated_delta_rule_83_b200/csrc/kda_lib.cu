@@ -122,6 +122,43 @@ kda_status make_bwd_plan(int B, int T, int H, int Hk, unsigned pro, int dk, int 
     return KDA_OK;
 }
 
+// The backward in a workspace of plan p: chunk table, then the kernels.  HEAD: one forget gate a head (log_alpha
+// [tokens][H]; dlog_alpha still has a value for each key channel).
+template <typename TIn, bool HEAD = false>
+cudaError_t run_backward(const void* q, const void* k, const void* v, const void* log_alpha, const float* beta,
+                         const float* S0, const int32_t* cu, const void* dout, const float* dS_final, void* dq, void* dk_out,
+                         void* dv_out, float* dlog_alpha, float* dbeta, float* dS0, int H, int Hk, unsigned pro, int dk,
+                         int dv, const BwdPlan& p, char* ws, cudaStream_t stream)
+{
+    WsHeader* hdr = (WsHeader*)ws;
+    int* off = (int*)(ws + sizeof(WsHeader));
+    const size_t units = (size_t)p.f.max_chunks * (size_t)H;
+    char* slots = ws + sizeof(WsHeader) + p.f.off_bytes;
+    char* states = slots + units * p.slot_bytes;
+    char* cot = states + units * p.state_bytes;
+    char* scr = cot + units * p.state_bytes;
+    char* fdo = scr + units * p.scr_bytes;  // F = Qg^T dO per chunk
+    char* acc = ws + round_up(sizeof(WsHeader) + p.f.off_bytes +
+                              units * (p.slot_bytes + 3 * p.state_bytes + p.scr_bytes), kAlign);
+    char* qn = acc + 2 * p.acc_bytes;  // prologue buffers (empty when their bit is off)
+    char* kn = qn + p.qk_bytes;
+    char* la_act = kn + p.qk_bytes;
+    char* beta_act = la_act + p.la_bytes;
+    {
+        LaunchScope ls("chunk_table", stream);
+        chunk_table_kernel<<<1, kTableThreads, 0, stream>>>(cu, p.f.N, p.f.Tseq, p.f.Ttot, hdr, off,
+                                                             off + p.f.N + 1);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    // the per-unit regions are indexed by (chunk, head) with the dense strides of the kernels
+    return launch_simt_backward<TIn, HEAD>(q, k, v, log_alpha, beta, S0, dout, dS_final, dq, dk_out, dv_out, dlog_alpha,
+                                           dbeta, dS0, hdr, off, cu, p.f.Tseq, p.f.N, H, Hk, pro, dk, dv,
+                                           p.f.max_chunks, p.f.Ttot, (float*)slots, (float*)states, (float*)cot,
+                                           (float*)scr, (float*)fdo, (float*)acc, (float*)(acc + p.acc_bytes), qn, kn,
+                                           (float*)la_act, (float*)beta_act, stream);
+}
+
 // Options of the extended entry points: Hk = q/k heads (0 -> H), prologue bits; reserved fields
 // must be zero.
 kda_status parse_options(const kda_options* opt, int H, int& Hk, unsigned& pro)
@@ -331,40 +368,11 @@ kda_status kda_chunk_bwd(const void* q, const void* k, const void* v, const void
     if (cu_seqlens && ((uintptr_t)cu_seqlens & 3u)) return KDA_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace % kAlign) || workspace_bytes < p.total_bytes) return KDA_ERR_WORKSPACE;
 
-    char* ws = (char*)workspace;
-    WsHeader* hdr = (WsHeader*)ws;
-    int* off = (int*)(ws + sizeof(WsHeader));
-    const size_t units = (size_t)p.f.max_chunks * (size_t)H;
-    char* slots = ws + sizeof(WsHeader) + p.f.off_bytes;
-    char* states = slots + units * p.slot_bytes;
-    char* cot = states + units * p.state_bytes;
-    char* scr = cot + units * p.state_bytes;
-    char* fdo = scr + units * p.scr_bytes;  // F = Qg^T dO per chunk
-    char* acc = ws + round_up(sizeof(WsHeader) + p.f.off_bytes +
-                              units * (p.slot_bytes + 3 * p.state_bytes + p.scr_bytes), kAlign);
-    char* qn = acc + 2 * p.acc_bytes;  // prologue buffers (empty when their bit is off)
-    char* kn = qn + p.qk_bytes;
-    char* la_act = kn + p.qk_bytes;
-    char* beta_act = la_act + p.la_bytes;
-    {
-        LaunchScope ls("chunk_table", stream);
-        chunk_table_kernel<<<1, kTableThreads, 0, stream>>>(cu_seqlens, p.f.N, p.f.Tseq, p.f.Ttot, hdr, off,
-                                                             off + p.f.N + 1);
-        if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
-    }
-    // the per-unit regions are indexed by (chunk, head) with the dense strides of the kernels
-    const cudaError_t e = (dt == KDA_BF16)
-        ? launch_simt_backward<__nv_bfloat16>(q, k, v, log_alpha, beta, S0, dout, dS_final, dq, dk_out, dv_out,
-                                              dlog_alpha, dbeta, dS0, hdr, off, cu_seqlens, p.f.Tseq, p.f.N, H, Hk,
-                                              pro, dk, dv, p.f.max_chunks, p.f.Ttot, (float*)slots, (float*)states,
-                                              (float*)cot, (float*)scr, (float*)fdo, (float*)acc,
-                                              (float*)(acc + p.acc_bytes), qn, kn, (float*)la_act,
-                                              (float*)beta_act, stream)
-        : launch_simt_backward<float>(q, k, v, log_alpha, beta, S0, dout, dS_final, dq, dk_out, dv_out, dlog_alpha,
-                                      dbeta, dS0, hdr, off, cu_seqlens, p.f.Tseq, p.f.N, H, Hk, pro, dk, dv,
-                                      p.f.max_chunks, p.f.Ttot, (float*)slots, (float*)states, (float*)cot,
-                                      (float*)scr, (float*)fdo, (float*)acc, (float*)(acc + p.acc_bytes), qn,
-                                      kn, (float*)la_act, (float*)beta_act, stream);
+    const cudaError_t e = dt == KDA_BF16
+        ? run_backward<__nv_bfloat16>(q, k, v, log_alpha, beta, S0, cu_seqlens, dout, dS_final, dq, dk_out, dv_out,
+                                      dlog_alpha, dbeta, dS0, H, Hk, pro, dk, dv, p, (char*)workspace, stream)
+        : run_backward<float>(q, k, v, log_alpha, beta, S0, cu_seqlens, dout, dS_final, dq, dk_out, dv_out, dlog_alpha,
+                              dbeta, dS0, H, Hk, pro, dk, dv, p, (char*)workspace, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

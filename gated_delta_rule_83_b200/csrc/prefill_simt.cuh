@@ -19,9 +19,13 @@
 // some channel decays by more than e^-160 uses the exact per-element factor instead (never larger
 // than 1), so no gate value can overflow.  Padding rows of a partial chunk are identity steps
 // (k = q = v = 0, log_alpha = 0, beta = 0).
+//
+// HEAD (one forget gate a head, log_alpha [tokens][H]): the decays D_ri = e^{g_r - g_i} multiply the plain
+// products k_r.k_i and q_r.k_i, g being a pair of floats; the rest is the same.
 #pragma once
 
 #include "common.cuh"
+#include "head_gate.cuh"
 #include "profile.cuh"
 
 namespace kda {
@@ -188,7 +192,7 @@ __device__ void simt_intra_wuv_tc(const float* sT, const float* sKt, const __nv_
                                   int L, int H, int h, float* tiles, float* __restrict__ gW, float* __restrict__ gUv,
                                   uint32_t* s_tm, uint64_t* s_mb, uint32_t phase);
 
-template <typename TIn, bool TC = false>
+template <typename TIn, bool TC = false, bool HEAD = false>
 __global__ void __launch_bounds__(kSimtThreads)
 simt_intra_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
                   const void* __restrict__ log_alpha, const float* __restrict__ beta, const WsHeader* __restrict__ hdr,
@@ -221,10 +225,14 @@ simt_intra_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TI
     __shared__ int s_wide;
     __shared__ uint32_t s_tm;  // TC: TMEM base address and the MMA-completion barrier
     __shared__ uint64_t s_mb;
+    __shared__ __align__(8) float s_g[HEAD ? kChunk : 2], s_gl[HEAD ? kChunk : 2];  // g of the head, hi + lo
     const int tr = tid >> 4, tc = tid & 15;
 
     if (tid == 0) s_wide = 0;
     if constexpr (TC) simt_intra_tc_setup(&s_tm, &s_mb);
+    if constexpr (HEAD) {
+        if (tid < 32) load_scalars(reinterpret_cast<const float*>(log_alpha), beta, t0, L, H, h, s_g, s_gl, sb);
+    }
     // 8 consecutive channels per thread and step (16- or 32-byte loads); rows past the end read as 0
     for (int e = tid; e < kChunk * dk / 8; e += kSimtThreads) {
         const int r = e / (dk / 8), c = 8 * (e % (dk / 8));
@@ -234,16 +242,18 @@ simt_intra_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TI
             const size_t qi = ((size_t)(t0 + r) * Hk + h / (H / Hk)) * dk + c;  // q/k head of value head h
             load8(k + qi, kv);
             load8(q + qi, qv);
-            if (pro & KDA_PROLOGUE_GATE_BF16) load8(reinterpret_cast<const __nv_bfloat16*>(log_alpha) + gi, lv);
-            else load8(reinterpret_cast<const float*>(log_alpha) + gi, lv);
-            if (pro & KDA_PROLOGUE_GATE_LOGITS)  // rows past the end stay 0 (identity)
-                for (int m = 0; m < 8; ++m) lv[m] = log_sigmoid_f(lv[m]);
+            if constexpr (!HEAD) {
+                if (pro & KDA_PROLOGUE_GATE_BF16) load8(reinterpret_cast<const __nv_bfloat16*>(log_alpha) + gi, lv);
+                else load8(reinterpret_cast<const float*>(log_alpha) + gi, lv);
+                if (pro & KDA_PROLOGUE_GATE_LOGITS)  // rows past the end stay 0 (identity)
+                    for (int m = 0; m < 8; ++m) lv[m] = log_sigmoid_f(lv[m]);
+            }
         }
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
             sk[r * LK + c + m] = kv[m];
             sq[r * LK + c + m] = qv[m];
-            sg[r * LK + c + m] = lv[m];
+            if constexpr (!HEAD) sg[r * LK + c + m] = lv[m];
         }
     }
     for (int e = tid; e < kChunk * dv / 8; e += kSimtThreads) {
@@ -253,7 +263,7 @@ simt_intra_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TI
 #pragma unroll
         for (int m = 0; m < 8; ++m) sv[r * LV + c + m] = vv[m];
     }
-    for (int r = tid; r < kChunk; r += kSimtThreads) {
+    for (int r = tid; r < kChunk && !HEAD; r += kSimtThreads) {
         float b = 0.f;
         if (r < L) {
             b = beta[(size_t)(t0 + r) * H + h];
@@ -280,7 +290,7 @@ simt_intra_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TI
     }
 
     // cumulative gate per channel; reference point = centre of the channel's range
-    for (int c = tid; c < dk; c += kSimtThreads) {
+    for (int c = tid; c < dk && !HEAD; c += kSimtThreads) {
         float acc = 0.f, lo = 0.f, hi = 0.f;
         for (int r = 0; r < kChunk; ++r) {
             acc += sg[r * LK + c];
@@ -305,19 +315,21 @@ simt_intra_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TI
     // gated operands that never overflow (every exponent <= 0)
     for (int e = tid; e < kChunk * dk; e += kSimtThreads) {
         const int r = e / dk, c = e % dk, x = r * LK + c;
-        const float gl = sg[(kChunk - 1) * LK + c];
-        const float eg = fast_exp(sg[x]);
+        const float gl = HEAD ? 0.f : sg[(kChunk - 1) * LK + c];
+        const float eg = HEAD ? tc::ex2_approx(s_g[r]) : fast_exp(sg[x]);
         gQ[e] = sq[x] * eg;
-        gKd[e] = sk[x] * fast_exp(gl - sg[x]);
+        gKd[e] = sk[x] * (HEAD ? head_decay(s_g, s_gl, kChunk - 1, r) : fast_exp(gl - sg[x]));
         sKt[x] = sk[x] * eg;
-        if (r == 0) gGam[c] = fast_exp(gl);
+        if (r == 0) gGam[c] = HEAD ? tc::ex2_approx(s_g[kChunk - 1]) : fast_exp(gl);
     }
     __syncthreads();
 
     const bool wide = s_wide != 0;
     if (!wide) {
         // factorised form: e^{g_r - g_i} = e^{g_r - ref} e^{ref - g_i}, both factors within e^{+-80}
-        for (int e = tid; e < kChunk * dk; e += kSimtThreads) {
+        // (HEAD: the plain products, decayed below; Kb is k)
+        const float* skb = HEAD ? sk : sg;
+        for (int e = tid; e < kChunk * dk && !HEAD; e += kSimtThreads) {
             const int r = e / dk, c = e % dk, x0 = r * LK + c;
             const float x = sg[x0] - sref[c];
             const float kv = sk[x0];
@@ -338,7 +350,7 @@ simt_intra_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TI
             for (int a = 0; a < 4; ++a) {
                 kf[a] = sk[(tr + 16 * a) * LK + c];
                 qf[a] = sq[(tr + 16 * a) * LK + c];
-                kb[a] = sg[(tc + 16 * a) * LK + c];
+                kb[a] = skb[(tc + 16 * a) * LK + c];
             }
 #pragma unroll
             for (int a = 0; a < 4; ++a)
@@ -353,6 +365,11 @@ simt_intra_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TI
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int r = tr + 16 * a, i = tc + 16 * b;
+                if constexpr (HEAD) {
+                    const float D = head_decay(s_g, s_gl, r, i);
+                    a_[a][b] *= D;
+                    p_[a][b] *= D;
+                }
                 sA[r * L64 + i] = (i < r) ? sb[r] * a_[a][b] : 0.f;
                 sP[r * L64 + i] = (i <= r) ? p_[a][b] : 0.f;
             }
@@ -536,21 +553,21 @@ inline size_t simt_inter_smem(int dk, int dv)
                             2 * kChunk * kSimtNV + dk);
 }
 
-template <typename TIn>
+template <typename TIn, bool HEAD = false>
 cudaError_t launch_simt_prefill(const void* q, const void* k, const void* v, const void* la, const float* beta,
                                 const float* S0, float* S_final, void* out, const WsHeader* hdr, const int* off,
                                 const int32_t* cu, int Tseq, int N, int H, int Hk, unsigned pro, int dk, int dv,
                                 int max_chunks, float* slots, cudaStream_t stream)
 {
     const size_t smA = simt_intra_smem(dk, dv), smB = simt_inter_smem(dk, dv);
-    cudaError_t e = cudaFuncSetAttribute(simt_intra_kernel<TIn>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smA);
+    cudaError_t e = cudaFuncSetAttribute(simt_intra_kernel<TIn, false, HEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smA);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(dk == 128 ? simt_inter_kernel<TIn, 128> : simt_inter_kernel<TIn, 64>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smB);
     if (e != cudaSuccess) return e;
     if (max_chunks > 0) {
         LaunchScope ls("simt_intra", stream);
-        simt_intra_kernel<TIn><<<dim3(max_chunks, H), kSimtThreads, smA, stream>>>(
+        simt_intra_kernel<TIn, false, HEAD><<<dim3(max_chunks, H), kSimtThreads, smA, stream>>>(
             (const TIn*)q, (const TIn*)k, (const TIn*)v, la, beta, hdr, off, cu, Tseq, N, H, Hk, pro, dk, dv, slots);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
