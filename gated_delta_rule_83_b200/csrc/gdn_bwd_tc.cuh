@@ -10,10 +10,11 @@
 //     dbeta_i = dR_i.v_i - 2^g_i k_i.(dR S^T)_i + (E . k k^T) row sum
 //     dg_i = q_i.dq_i + k_i.ka_i - k_i.kb_i,  dg_C += sum_j w_j k_j.(U dS'^T)_j + 2^g_C <S, dS'>
 //     dlog_alpha_i = sum of dg_m over m >= i in the chunk
-// of which PD's diagonal cancels in each dg_i and the terms of w and U with the sum at C; they are left out, so that
-// a gate that acts on a zero state has a gradient of zero (not of 1e-6):
+// of which PD's diagonal cancels in each dg_i and the terms of w and U with the sum at C; they are left out:
 //     dlog_alpha_i = sum over m >= i of [q.dq + k.ka - k.kb without them]_m + sum over m < i of w_m k_m.(U dS'^T)_m
 //                    + 2^g_C <S, dS'>
+// Without a start state a sequence's first gate multiplies zeros.  Its gradient is written as zero, where the sums
+// would leave their rounding (1e-5).
 // Three passes: per-chunk matrices (gdn_prep); side by side the forward states again and the reverse chain
 // for dS' and dR (in segments, with a pass for their ends before); one CTA a (chunk, head) for the gradients.
 // dg is taken from row products of terms that belong to this chunk, never from a sum over the whole sequence,
@@ -399,7 +400,7 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                      __nv_bfloat16* __restrict__ dk, float* __restrict__ dq_acc, float* __restrict__ dk_acc,
                      float* __restrict__ dla, float* __restrict__ dbeta, const WsHeader* __restrict__ hdr,
                      const int* __restrict__ off, const int32_t* __restrict__ cu, int Tseq, int N, int H, int G, int dkw,
-                     const uint8_t* __restrict__ images)
+                     bool start, const uint8_t* __restrict__ images)
 {
     extern __shared__ uint8_t smem_raw[];
     if (cu && (hdr->bad || (long long)blockIdx.x >= (long long)hdr->total_chunks * H)) return;
@@ -739,8 +740,9 @@ gdn_bwd_grads_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         for (int i = 0; i < 8; ++i) end += s_sds[i];
         end *= ex2_approx(s_g[63]);
         const size_t o = (size_t)(t0 + 2 * lane) * H + h;
+        const bool on_zero = !start && lane == 0 && t0 == (cu ? (long long)cu[n] : (long long)n * Tseq);
         if (2 * lane < L) {
-            dla[o] = (s + ahead) + end;
+            dla[o] = on_zero ? 0.f : (s + ahead) + end;
             dbeta[o] = sum4(2, 2 * lane);
         }
         if (2 * lane + 1 < L) {
@@ -845,7 +847,7 @@ inline cudaError_t launch_bwd(const void* q, const void* k, const void* v, const
         LaunchScope ls("gdn_bwd_grads", stream);
         gdn_bwd_grads_kernel<<<(unsigned)units, kGThreads, kGSmem, stream>>>(
             tq, tk, tv, tdo, la, beta, (__nv_bfloat16*)dq, (__nv_bfloat16*)dk, dq_acc, dk_acc, dla, dbeta, hdr, off, cu,
-            Tseq, N, H, H / Hk, dkw, images);
+            Tseq, N, H, H / Hk, dkw, S0 != nullptr, images);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (grouped) {

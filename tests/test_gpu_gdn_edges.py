@@ -7,6 +7,7 @@ import torch
 from tests.test_gpu_gdn import DEV, check, make, ref_bwd, ref_fwd, run_bwd, run_fwd
 
 pytestmark = pytest.mark.gpu
+BOTH = [torch.bfloat16, torch.float32]
 GRADS = ("dq", "dk", "dv", "dlog_alpha", "dbeta", "dS0")
 
 
@@ -32,3 +33,20 @@ def test_resets_through_a_chunk(dt, dk, dv, every, gate):
         check(g[x], ref[x], dt, x)
     for x in GRADS[:-1]:
         check(g[x][:, late], ref[x][:, at], dt, x + ", late tokens")
+
+
+@pytest.mark.parametrize("dt", BOTH)
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
+@pytest.mark.parametrize("kw", [dict(T=2, B=3), dict(T=64, B=2), dict(T=130, B=2), dict(lens=[2, 0, 64, 1, 130, 65])])
+def test_the_first_gate_has_no_gradient_without_a_start_state(dt, dk, dv, kw):
+    """It multiplies zeros, whatever follows: exactly zero; the other gates' gradients are right."""
+    d = make(44, dt, 4, 2, dk, dv, s0=False, **kw)
+    g, ref = run_bwd(d), ref_bwd(d)
+    check(g["dlog_alpha"], ref["dlog_alpha"], dt, "dlog_alpha")
+    if "lens" in kw:
+        first = [int(t) for t, n in zip(d["cu"][:-1].tolist(), kw["lens"]) if n]
+    else:
+        first = [0]
+    assert not g["dlog_alpha"][:, first].any()
+    if d["q"].shape[1] > 2:
+        assert g["dlog_alpha"].any()
