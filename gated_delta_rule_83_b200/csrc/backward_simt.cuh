@@ -959,15 +959,16 @@ bwd_gate_act_kernel(const void* __restrict__ la, bool la16, bool logits, float* 
 }
 
 // dq, dk of the raw q/k heads: sum over the G value heads of each q/k head (value head h reads q/k
-// head h / G; rows t*H + hk*G + g are consecutive in acc), then, with the norm, its chain rule
+// head h / G; rows t*H + hk*G + g are consecutive in acc), then, with the norm, its chain rule.
+// Malformed offsets: acc holds nothing, and nothing is written.
 template <typename TIn>
 __global__ void __launch_bounds__(32 * kRowWarps)
 bwd_qk_grad_kernel(const float* __restrict__ acc, const TIn* __restrict__ x_raw, TIn* __restrict__ out, long long rows,
-                   int G, int dk, bool l2norm)
+                   int G, int dk, bool l2norm, const WsHeader* __restrict__ hdr)
 {
     const long long row = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, per = dk / 32;
-    if (row >= rows) return;
+    if (row >= rows || hdr->bad) return;
     float g[4], x[4], ss = 0.f, dot = 0.f;
     for (int m = 0; m < per; ++m) {
         const int c = lane + 32 * m;
@@ -990,12 +991,15 @@ bwd_qk_grad_kernel(const float* __restrict__ acc, const TIn* __restrict__ x_raw,
     for (int m = 0; m < per; ++m) out[(size_t)row * dk + lane + 32 * m] = from_f32<TIn>(g[m]);
 }
 
-// in place: dlog_alpha *= sigmoid(-a) for gate logits a; dbeta *= sigmoid(b) (1 - sigmoid(b))
+// in place: dlog_alpha *= sigmoid(-a) for gate logits a; dbeta *= sigmoid(b) (1 - sigmoid(b)); not with malformed
+// offsets, where neither was written
 __global__ void __launch_bounds__(256)
 bwd_gate_act_grad_kernel(const void* __restrict__ la, bool la16, float* __restrict__ dla, long long n_la,
-                         const float* __restrict__ beta, float* __restrict__ dbeta, long long n_beta)
+                         const float* __restrict__ beta, float* __restrict__ dbeta, long long n_beta,
+                         const WsHeader* __restrict__ hdr)
 {
     const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (hdr->bad) return;
     if (dla && e < n_la) {
         const float a = la16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(la)[e])
                              : reinterpret_cast<const float*>(la)[e];
@@ -1207,9 +1211,9 @@ cudaError_t launch_simt_backward(const void* q, const void* k, const void* v, co
             const long long rows = Ttot * Hk, blocks = (rows + kRowWarps - 1) / kRowWarps;
             if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
             bwd_qk_grad_kernel<TIn><<<(unsigned)blocks, 32 * kRowWarps, 0, stream>>>(
-                dq_acc, (const TIn*)q_raw, (TIn*)dq, rows, H / Hk, dk, l2norm);
+                dq_acc, (const TIn*)q_raw, (TIn*)dq, rows, H / Hk, dk, l2norm, hdr);
             bwd_qk_grad_kernel<TIn><<<(unsigned)blocks, 32 * kRowWarps, 0, stream>>>(
-                dk_acc, (const TIn*)k_raw, (TIn*)dk_out, rows, H / Hk, dk, l2norm);
+                dk_acc, (const TIn*)k_raw, (TIn*)dk_out, rows, H / Hk, dk, l2norm, hdr);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
         if (pro_raw & (KDA_PROLOGUE_GATE_LOGITS | KDA_PROLOGUE_BETA_LOGITS)) {
@@ -1220,7 +1224,7 @@ cudaError_t launch_simt_backward(const void* q, const void* k, const void* v, co
             const bool gl = (pro_raw & KDA_PROLOGUE_GATE_LOGITS) != 0, bl = (pro_raw & KDA_PROLOGUE_BETA_LOGITS) != 0;
             bwd_gate_act_grad_kernel<<<(unsigned)blocks, 256, 0, stream>>>(
                 la_raw, (pro_raw & KDA_PROLOGUE_GATE_BF16) != 0, gl ? dla : nullptr, n_la, beta_raw,
-                bl ? dbeta : nullptr, n_b);
+                bl ? dbeta : nullptr, n_b, hdr);
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
     }

@@ -4,7 +4,7 @@ those of test_gpu_gdn."""
 import pytest
 import torch
 
-from tests.test_gpu_gdn import DEV, check, make, ref_bwd, ref_fwd, run_bwd, run_fwd
+from tests.test_gpu_gdn import DEV, check, kda, make, ref_bwd, ref_fwd, run_bwd, run_fwd
 
 pytestmark = pytest.mark.gpu
 BOTH = [torch.bfloat16, torch.float32]
@@ -50,3 +50,42 @@ def test_the_first_gate_has_no_gradient_without_a_start_state(dt, dk, dv, kw):
     assert not g["dlog_alpha"][:, first].any()
     if d["q"].shape[1] > 2:
         assert g["dlog_alpha"].any()
+
+
+def _untouched(call, like):
+    """A call with malformed offsets and all gradients given: none is written and the fault is reported."""
+    m = kda()
+    mine = {x: torch.full_like(y, 3.0) for x, y in like.items()}
+    call(mine)
+    with pytest.raises(m.KdaError) as e:
+        m.check()
+    assert e.value.code == 6
+    for x, y in mine.items():
+        assert (y == 3.0).all(), x
+
+
+@pytest.mark.parametrize("dt", BOTH)
+@pytest.mark.parametrize("dk", [64, 128])
+def test_bad_offsets_leave_every_gradient(dt, dk):
+    d = make(41, dt, 4, 2, dk, dk, lens=[30, 30, 40])
+    d["cu"] = torch.tensor([0, 50, 40, 100], dtype=torch.int32, device=DEV)
+    _untouched(lambda mine: kda().gdn_chunk_bwd(d["q"], d["k"], d["v"], d["log_alpha"], d["beta"], d["dout"],
+                                                S0=d["S0"], cu_seqlens=d["cu"], grads=mine),
+               {"dq": d["q"], "dk": d["k"], "dv": d["v"], "dlog_alpha": d["log_alpha"], "dbeta": d["beta"],
+                "dS0": d["S0"]})
+
+
+@pytest.mark.parametrize("dt", BOTH)
+@pytest.mark.parametrize("prologue", [0, "all"])
+def test_bad_offsets_leave_every_gradient_of_channel_gates(dt, prologue):
+    """The form with a gate a key channel: shared heads and the input prologue add passes behind the chunks'."""
+    m = kda()
+    d = make(42, dt, 4, 2, 128, 128, lens=[30, 30, 40])
+    la = torch.randn(1, 100, 4, 128, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    pro = 0
+    if prologue:
+        pro = m.PROLOGUE_L2NORM_QK | m.PROLOGUE_GATE_LOGITS | m.PROLOGUE_BETA_LOGITS
+    d["cu"] = torch.tensor([0, 50, 40, 100], dtype=torch.int32, device=DEV)
+    _untouched(lambda mine: m.chunk_bwd(d["q"], d["k"], d["v"], la if prologue else -la.abs(), d["beta"], d["dout"],
+                                        S0=d["S0"], cu_seqlens=d["cu"], grads=mine, prologue=pro),
+               {"dq": d["q"], "dk": d["k"], "dv": d["v"], "dlog_alpha": la, "dbeta": d["beta"], "dS0": d["S0"]})
