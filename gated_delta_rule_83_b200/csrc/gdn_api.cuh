@@ -149,7 +149,6 @@ extern "C" kda_status kda_gdn_chunk_bwd(const void* q, const void* k, const void
                                               (uint8_t*)(ws + sizeof(WsHeader) + f.off_bytes), stream);
         return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
-    if (!all_aligned16({beta, dbeta})) return KDA_ERR_INVALID_ARG;
     float* dgate = (float*)((char*)workspace + round_up(p.b.total_bytes, kAlign));
     cudaError_t e = run_backward<float, true>(q, k, v, log_alpha, beta, S0, cu_seqlens, dout, dS_final, dq, dk_out, dv_out,
                                               dgate, dbeta, dS0, H, Hk, 0u, dk, dv, p.b, (char*)workspace, stream);

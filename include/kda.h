@@ -361,8 +361,8 @@ kda_status kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const 
  *   dq, dk [B, T, Hk, dk] dt (summed over the value heads of a q/k head);  dv [B, T, H, dv] dt;
  *   dlog_alpha, dbeta [B, T, H] fp32;  dS0 [N, H, dk, dv] fp32 or NULL (not wanted).  All written whole.
  *   dout is [B, T, H, dv] dt; dS_final [N, H, dk, dv] fp32 or NULL (= 0).  The other arguments are those
- * of the forward call (fp32: beta and dbeta 16-byte aligned).  No output may overlap an input.  Workspace,
- * errors and asynchrony as kda_chunk_bwd.
+ * of the forward call; log_alpha, beta and their gradients 4-byte aligned.  No output may overlap an input.
+ * Workspace, errors and asynchrony as kda_chunk_bwd.
  */
 kda_status kda_gdn_chunk_bwd_workspace_size(int B, int T, int H, int Hk, int dk, int dv, int varlen, int num_seqs,
                                             kda_dtype dt, size_t* bytes);

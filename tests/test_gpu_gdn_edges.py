@@ -89,3 +89,22 @@ def test_bad_offsets_leave_every_gradient_of_channel_gates(dt, prologue):
     _untouched(lambda mine: m.chunk_bwd(d["q"], d["k"], d["v"], la if prologue else -la.abs(), d["beta"], d["dout"],
                                         S0=d["S0"], cu_seqlens=d["cu"], grads=mine, prologue=pro),
                {"dq": d["q"], "dk": d["k"], "dv": d["v"], "dlog_alpha": la, "dbeta": d["beta"], "dS0": d["S0"]})
+
+
+@pytest.mark.parametrize("dt", BOTH)
+def test_scalars_may_start_at_any_element(dt):
+    """log_alpha, beta and their gradients lie one element into a buffer, as a slice of a larger tensor does."""
+    d = make(40, dt, 3, 1, 64, 128, lens=[70, 1, 20])
+    want = (run_fwd(d), run_bwd(d))
+
+    def behind(x):
+        y = torch.empty(x.numel() + 1, device=DEV)[1:].view(x.shape)
+        return y.copy_(x)
+
+    e = dict(d, log_alpha=behind(d["log_alpha"]), beta=behind(d["beta"]))
+    mine = {x: behind(torch.zeros_like(d["beta"])) for x in ("dlog_alpha", "dbeta")}
+    out, S = run_fwd(e)
+    g = run_bwd(e, grads=mine)
+    assert torch.equal(out, want[0][0]) and torch.equal(S, want[0][1])
+    assert g["dbeta"] is mine["dbeta"] and g["dlog_alpha"] is mine["dlog_alpha"]
+    assert all(torch.equal(g[x], want[1][x]) for x in GRADS)
