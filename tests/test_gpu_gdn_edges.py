@@ -4,7 +4,7 @@ those of test_gpu_gdn."""
 import pytest
 import torch
 
-from tests.test_gpu_gdn import DEV, check, kda, make, ref_bwd, ref_fwd, run_bwd, run_fwd
+from tests.test_gpu_gdn import DEV, check, kda, make, ref_bwd, ref_fwd, rel, run_bwd, run_fwd
 
 pytestmark = pytest.mark.gpu
 BOTH = [torch.bfloat16, torch.float32]
@@ -108,3 +108,68 @@ def test_scalars_may_start_at_any_element(dt):
     assert torch.equal(out, want[0][0]) and torch.equal(S, want[0][1])
     assert g["dbeta"] is mine["dbeta"] and g["dlog_alpha"] is mine["dlog_alpha"]
     assert all(torch.equal(g[x], want[1][x]) for x in GRADS)
+
+
+def launched(call):
+    """The call's result and the names of the kernels it launched."""
+    m = kda()
+    m.profile_begin()
+    try:
+        got = call()
+    finally:
+        names = set(m.profile_end())
+    m.check()
+    return got, names
+
+
+# lengths, heads, q/k heads, dk, dv, start state
+CUT = [
+    dict(lens=[6000, 10, 0, 3000, 0], H=1, Hk=1, dk=128, dv=128),
+    dict(lens=[0, 6000, 0, 70, 5100, 1], H=2, Hk=1, dk=128, dv=128),
+    dict(lens=[2049, 64, 0, 5000], H=2, Hk=2, dk=64, dv=128, s0=False),
+    dict(lens=[63] * 14 + [0] * 10 + [50000] + [1] * 8 + [46000, 130], H=1, Hk=1, dk=64, dv=64),
+    dict(lens=[5000], H=2, Hk=2, dk=128, dv=64),
+    dict(T=3300, B=2, H=2, Hk=1, dk=128, dv=128),
+    dict(T=4097, B=3, H=1, Hk=1, dk=64, dv=64, s0=False),
+    dict(T=2900, B=2, H=1, Hk=1, dk=64, dv=128),
+]
+
+
+@pytest.mark.parametrize("case", CUT, ids=[",".join(f"{k}={v}" for k, v in c.items())[:90] for c in CUT])
+def test_sequences_cut_into_segments(case):
+    """Packed sequences and batches that are cut, forward and backward; the state passed in place too.  Each call's
+    launches show that it was: the ends of the segments and the join are kernels of their own.
+
+    Gates of 1e-4 a token and small beta, so that a segment's start state still weighs e^-0.5 at its end: a token takes
+    beta / dk off the state, at beta = 0.1 and dk = 128 a chunk 0.05 and the gates 0.01, a memory of 1 / 0.06 = 17
+    chunks.  The errors of so many chunks may add where their parts of the result add as squares: sqrt(17) < 2^2.1 of
+    the tolerance of one chunk, 2^-13, so 2^-10.9."""
+    c = dict(case)
+    d = make(45, torch.bfloat16, c.pop("H"), c.pop("Hk"), c.pop("dk"), c.pop("dv"), gate=9.0, **c)
+    d["beta"] *= 0.2
+
+    def check(got, want, name):
+        tol = 2.0 ** -10.9 + (2.0 ** -8 if got.dtype == torch.bfloat16 else 0.0)
+        assert rel(got, want) <= tol, f"{name}: {rel(got, want):.3e} > {tol:.3e}"
+
+    (out, S), names = launched(lambda: run_fwd(d))
+    assert {"gdn_ends", "gdn_join", "gdn_chain"} <= names
+    o_ref, s_ref = ref_fwd(d)
+    check(out, o_ref, "out")
+    check(S, s_ref, "S")
+    if d["S0"] is not None:
+        mine = d["S0"].clone()
+        m = kda()
+        out2, S2 = m.gdn_chunk_fwd(d["q"], d["k"], d["v"], d["log_alpha"], d["beta"], S0=mine, S_final=mine,
+                                   cu_seqlens=d["cu"])
+        m.check()
+        assert S2 is mine and torch.equal(out, out2) and torch.equal(S, mine)
+    g, names = launched(lambda: run_bwd(d))
+    assert {"gdn_bwd_ends", "gdn_join", "gdn_bwd_chains"} <= names
+    ref = ref_bwd(d)
+    for x in GRADS:
+        check(g[x], ref[x], x)
+    # each sequence's own state and its cotangent, as the norm over all hides a short one
+    for n in range(S.shape[0]):
+        check(S[n], s_ref[n], f"S[{n}]")
+        check(g["dS0"][n], ref["dS0"][n], f"dS0[{n}]")
