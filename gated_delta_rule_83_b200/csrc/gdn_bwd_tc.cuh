@@ -45,8 +45,8 @@ __device__ __forceinline__ uint64_t desc_image(uint32_t addr)
 //     dR = dU T      (12)          y = -beta 2^g dR
 //     D3 = dO^T (2^g q) + y k (8 of N = 128, under the making of dU; 16)     dS <- 2^g_C dS' + D3
 // TMEM columns: 0 D1 -> dU, 64 P^T dO, 128 dR -> y, 256 dS operand -> D3.
-// Bound like the forward chain, with one hand-over less: 3.9 us a chunk beside the forward chain of the same launch
-// (256 chunks of 64 + 64 CTAs 1.0 ms, 32 heads of 32K tokens in two segments), as both write their images.
+// Bound like the forward chain, with one hand-over less: 4.2 us a chunk beside the forward chain of the same launch
+// (256 chunks of 64 + 64 CTAs 1.06 ms, 32 heads of 32K tokens in two segments), as both write their images.
 // ----------------------------------------------------------------------------------------------------
 constexpr int kRThreads = 320;
 constexpr uint32_t kRK = 0, kRDo = 16384, kRGq = 32768, kRP = 65536, kRX = 81920, kRScal = 98304, kRStage = 99328;
@@ -348,7 +348,8 @@ __device__ __forceinline__ void reverse_body(const CUtensorMap* tm_k, const CUte
 }
 
 // Both chains of the backward in one launch, since neither needs the other and each alone leaves SMs idle: blocks
-// 0 .. nr - 1 reverse, the next nr forward, and with ENDS the next nr the forward transitions.
+// 0 .. nr - 1 reverse, the next nr forward, and with ENDS the next nr the forward transitions.  The joint kernel
+// spills: 184 bytes of a thread, with ENDS 104 (ptxas).
 template <bool ENDS>
 __global__ void __launch_bounds__(kRThreads, 1)
 gdn_bwd_chains_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -369,7 +370,7 @@ gdn_bwd_chains_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 //   first:  dO S^T and dR S^T (N = 128); dO U^T, dR U^T, k k^T and v dR^T (N = 64; of the last the diagonal)
 //   then, with dS' in S's place and the split PD and G in dO's and v's:  U dS'^T, PD k, G k, PD^T q + G^T k
 // 192 KB of operands and all of TMEM, one CTA an SM, so loads, MMAs and the conversions of a unit alternate: 32K
-// tokens x 32 heads 1.15 ms, 4.3 GB at 0.58 of the copy bandwidth, tensor pipe 44 % busy.  Fetching dS' and the next
+// tokens x 32 heads 1.24 ms, 4.3 GB at 0.54 of the copy bandwidth, tensor pipe 44 % busy.  Fetching dS' and the next
 // unit's images into L2 ahead saves 0.08; all of the next unit's operands cost 0.06..0.16 instead.
 // TMEM columns: 0 dO S^T, 128 dR S^T, 256 dO U^T, 320 dR U^T, 384 k k^T, 448 v dR^T; then 0 U dS'^T, 128 PD k,
 // 256 G k, 384 PD^T q + G^T k.

@@ -15,7 +15,9 @@
 // Precision.  X, P, Y, R, U and S are fp32; as tensor-core operands each is the sum of two bf16 parts
 // (hi + lo, 16 significant bits) and a product takes hi.hi + hi.lo + lo.hi, one pass less where the
 // other operand is an input.  Measured against 64 bits the states are off by 4..7e-6 where single bf16
-// operands give 3e-3.
+// operands give 3e-3.  A third part would make 24 bits of them, for one and a half to two times the MMAs of a chain
+// bound by their issue, and 576 TMEM columns where there are 512.  What is carried from chunk to chunk, S in the
+// threads' registers, and what a product sums are fp32.
 #pragma once
 
 #include <cuda.h>
@@ -440,12 +442,12 @@ gdn_prep_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 // other's, so that one's conversions run under the other's MMAs.  v enters as an operand, never through
 // registers.  What no thread waits for fills the tensor pipe's gaps: Dq under the making of R', R' Y^T under
 // that of U', v^T Y^T and the next chunk's v^T X^T under the state's update.
-// Bound by the round trips of the chain: 2.2..2.5 us a chunk with one CTA an SM (171 chunks of 96 CTAs 421 us, 32
+// Bound by the round trips of the chain: 2.5 us a chunk with one CTA an SM (171 chunks of 96 CTAs 427 us, 32
 // heads of 32K tokens in three segments), in which some 80 MMAs take one warp about 42 cycles each to issue and each of the
 // six hand-overs between MMA and conversions costs about 140 cycles.  Measured and not taken: a second issuing
 // warp (401 us there, but 340..355 against 323 for 8192 tokens x 16 heads, and spills in the backward's), four
 // conversion warpgroups, the next chunk's D1 from the Gram matrix of the keys (one hand-over less; 24 warps'
-// code leaves the instruction cache, 2.5 us).
+// code leaves the instruction cache, 2.5 us).  ptxas spills 28 bytes of a thread here and 84 without outputs.
 // TMEM columns: 0 D1 -> R', 64 Dq, 128 U, 192 Po, 256 S operand -> D3, 384 U'.
 // ----------------------------------------------------------------------------------------------------
 constexpr int kChainOut = 0;     // the prefill: writes out and S_final

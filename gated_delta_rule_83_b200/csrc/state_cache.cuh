@@ -10,8 +10,9 @@
 // Both are one streaming pass: 4 + 1 bytes an element.  A thread moves 8 consecutive values of a row (one
 // 32-byte access to the fp32 side, 8 bytes of codes) and holds kCacheRows rows in flight to cover the memory
 // latency; the state's loads are issued before the slot is known.  Bound by HBM: 192 states of 32 heads,
-// d = 128, read back in 67..70 us (0.92..0.96 of the copy bandwidth); 64 written in 37 us (0.70: the maximum has
-// to be known before the first code) and read in 28.
+// d = 128, read back in 67..70 us (0.92..0.96 of the copy bandwidth); 64 written in 37 us (0.70) and read in 28.  A
+// writing CTA loads its rows once and leaves, so no load of its own runs under its conversions, and a vote of the
+// whole CTA on repeated slots stands between the two; which costs how much is not measured.
 #pragma once
 
 #include "common.cuh"
@@ -44,7 +45,8 @@ __device__ __forceinline__ void st_stream8(float* p, const Float8& x)
                  : "memory");
 }
 
-// Eight CTAs an SM: 36.6 us for 64 states of 32 heads where five (43 registers, nothing spilled) take 40.3.
+// Eight CTAs an SM (32 registers, 40 bytes spilled): 36.6 us for 64 states of 32 heads where five (43 registers,
+// nothing spilled) take 40.3.
 template <int DV>
 __global__ void __launch_bounds__(kCacheThreads, 8)
 state_cache_write_kernel(const float* __restrict__ S, int8_t* __restrict__ cache, float* __restrict__ scale,
